@@ -409,6 +409,107 @@ int veda_attend_int8_paired(const veda_layout* layout, const void* q_codes, cons
                             const int64_t out_strides[3], int32_t h_total, const int32_t* heads, const float* q_row_sq,
                             const float* k_max_sq, void* workspace, size_t workspace_bytes, void* stream);
 
+/* ---------------------------------------------------------------- device: training the tile predictor
+ *
+ * The pages train the predictor against a teacher: "max-pooled full attention gives the tile-level
+ * distribution", and the predictor's scores learn it (their summary of the method; they print no training
+ * code). One step for a group of heads, with Q and K of a frozen model:
+ *
+ *     veda_gather (Q, K)     -> tile order and pooled features
+ *     veda_teacher           -> the teacher's tile logits; veda_select on them gives its top lists
+ *     veda_score_bias        -> the predictor's scores, with an optional learned relative position bias
+ *     veda_distill           -> loss of every query tile and the gradient of the scores
+ *     veda_score_backward    -> gradients of the two projections
+ *     veda_bias_backward     -> gradient of the bias
+ *
+ * All sums are fp32 or wider, nothing is atomic, and two calls on the same inputs give the same bits.
+ * Limits of every call here: 16384 video tiles and 65535 heads (VEDA_ERR_UNSUPPORTED beyond). Buffers need
+ * 16-byte alignment. Workspaces are caller-owned scratch, overwritten by the call and free for other use once
+ * its kernels have finished; two calls that may overlap need two. */
+
+/* The teacher's tile logits: full attention's logits, max-pooled over every pair of video tiles,
+ *     teacher[h, i, j] = max over real rows r of tile i and s of tile j of  D^-0.5 q_r . k_s - lse_r.
+ *  q_t, k_t  device bf16 [n_heads, N, D] tile order (from veda_gather).
+ *  row_lse   device fp32 [n_heads, S] at packed rows: the logarithm of each row's softmax sum, which makes the
+ *            entries logarithms of max-pooled attention probabilities; NULL pools the logits themselves (lse = 0). Rows whose lse is not finite are passed over, and so
+ *            are NaN logits; -inf where nothing is left.
+ *  teacher   device fp32 [n_heads, n_video, n_video] out. */
+int veda_teacher(const veda_layout* layout, const void* q_t, const void* k_t, int32_t n_heads, int32_t dim,
+                 const float* row_lse, float* teacher, void* stream);
+
+/* Buckets of the relative position bias. A video tile has a place (t, h, w) in its span's array of tiles. Per axis
+ * the distance |r|, r = key place - query place, falls into one of `reach` classes: the first e = (reach + 1) / 2
+ * hold one distance each (0 .. e - 1), class e + m starts at the smallest distance a with
+ * a^k >= e^(k - m) far^m, k = reach - e (geometric steps from e up to far_tiles), and the last class has no end. The axis index
+ * is the class for r <= 0 and reach - 1 + class for r > 0, so an axis has 2 reach - 1 of them; a pair's bucket is
+ * (index_t * (2 reach_h - 1) + index_h) * (2 reach_w - 1) + index_w. Two more buckets hold the pairs of tiles of
+ * different spans: the key's span before the query's, then behind it.
+ * reach in [1, 16], far_tiles in ((reach + 1) / 2, 32767], per axis t, h, w; at most 4096 buckets. */
+typedef struct {
+    int32_t reach[3];
+    int32_t far_tiles[3];
+} veda_bias_spec;
+
+/* Number of buckets (host). */
+int veda_bias_buckets(const veda_bias_spec* spec, int32_t* n_buckets);
+
+/* The bucket of every (query tile, key tile) pair: host int32 [n_video * n_video], row-major. */
+int veda_bias_index(const veda_layout* layout, const veda_bias_spec* spec, int32_t* index);
+
+/* veda_score's logits with the bias of each pair's bucket added,
+ *     scores[h, i, j] = q_hat_i . k_hat_j / sqrt(D) + bias[h, bucket(i, j)],
+ * keeping the projected features for veda_score_backward.
+ *  spec, bias  the buckets, and device fp32 [n_heads, buckets]; both NULL: no bias.
+ *  hats        device fp32 [2, n_heads, n_video, D] out: q_hat, then k_hat.
+ *  workspace   at least veda_score_bias_workspace_bytes().
+ * Other arguments and errors as veda_score. */
+size_t veda_score_bias_workspace_bytes(const veda_layout* layout, int32_t n_heads, int32_t dim);
+int veda_score_bias(const veda_layout* layout, const float* feats_q, const float* feats_k, int32_t n_heads, int32_t dim,
+                    const float* proj_q, const float* proj_k, const veda_bias_spec* spec, const float* bias, float* hats,
+                    void* workspace, size_t workspace_bytes, float* scores, void* stream);
+
+/* Gradient of the bias: d_bias[h, b] = sum of d_scores[h, i, j] over the pairs of bucket b.
+ *  d_scores   device fp32 [n_heads, n_video, n_video].
+ *  d_bias     device fp32 [n_heads, buckets] out (overwritten; a bucket without a pair gets 0).
+ *  workspace  at least veda_bias_backward_workspace_bytes(). */
+size_t veda_bias_backward_workspace_bytes(const veda_layout* layout, int32_t n_heads, const veda_bias_spec* spec);
+int veda_bias_backward(const veda_layout* layout, const float* d_scores, int32_t n_heads, const veda_bias_spec* spec,
+                       void* workspace, size_t workspace_bytes, float* d_bias, void* stream);
+
+/* Distillation from the teacher's top logits, loss and gradient in one pass. Per head and query tile,
+ *     p = softmax(t / tau) over the row's list,  q = softmax(s / tau) over all n_video columns,
+ *     loss = w sum_list p (log p - log q),       d_scores = (w / tau) (q - p),
+ * the gradient of the sum of all losses with respect to the scores (no tau^2: put it into w).
+ *  scores      device fp32 [n_heads, n_video, n_video].
+ *  t_idx       device int32 [n_heads, n_video, width]: ascending tile ids, as veda_select writes them
+ *              (width = max_kept); ids from n_video on (global tiles) are passed over.
+ *  t_cnt       device int32 [n_heads, n_video]: entries of each list, at most width.
+ *  t_val       the teacher's logits: device fp32 [n_heads, n_video, width], one per entry of t_idx, or with
+ *              by_column != 0 [n_heads, n_video, n_video] (veda_teacher's output), read at the listed columns.
+ *  tau         temperature, > 0.
+ *  row_weight  device fp32 [n_heads, n_video], or NULL for 1: w, for instance 1 / rows for a mean.
+ *  loss        device fp32 [n_heads, n_video] out.
+ *  d_scores    device fp32 [n_heads, n_video, n_video] out, or NULL for the loss alone; must not overlap scores.
+ * A row without a target (an empty list, or -inf at every entry of it) or without a score above -inf gets loss 0
+ * and gradient 0. A listed -inf carries no mass; a score of -inf has q = 0, and loss +inf where the teacher has
+ * mass there. NaN, and +inf scores, give NaN in their row. A list that is not ascending, leaves [0, n_tiles) or is longer than width
+ * is cut at its first bad entry, and veda_sync_status reports VEDA_ERR_BAD_LIST. */
+int veda_distill(const veda_layout* layout, const float* scores, int32_t n_heads, const int32_t* t_idx,
+                 const float* t_val, const int32_t* t_cnt, int32_t width, int32_t by_column, float tau,
+                 const float* row_weight, float* loss, float* d_scores, void* stream);
+
+/* Gradients of the projections from the gradient of the scores,
+ *     dq_hat = d_scores k_hat / sqrt(D),  dk_hat = d_scores^T q_hat / sqrt(D),
+ *     d_proj_q = feats_q^T dq_hat,        d_proj_k = feats_k^T dk_hat
+ * (the residual feats[:, :D] of the projected features has no parameters).
+ *  hats                device fp32 [2, n_heads, n_video, D] (from veda_score_bias on the same features).
+ *  d_proj_q, d_proj_k  device fp32 [n_heads, 3D, D] out (overwritten).
+ *  workspace           at least veda_score_backward_workspace_bytes(). */
+size_t veda_score_backward_workspace_bytes(const veda_layout* layout, int32_t n_heads, int32_t dim);
+int veda_score_backward(const veda_layout* layout, const float* feats_q, const float* feats_k, int32_t n_heads,
+                        int32_t dim, const float* hats, const float* d_scores, float* d_proj_q, float* d_proj_k,
+                        void* workspace, size_t workspace_bytes, void* stream);
+
 /* Synchronizes `stream`, then reads and clears this device's latched kernel error word.
  * Returns VEDA_OK, VEDA_ERR_TIMEOUT, VEDA_ERR_BAD_LIST or VEDA_ERR_CUDA. */
 int veda_sync_status(void* stream);

@@ -12,6 +12,9 @@ from ._lib import (  # noqa: F401
     veda_score_noalloc, veda_score_workspace_bytes, veda_select, veda_set_wait_timeout_ns, veda_sync_status,
     veda_quantize_fp8, veda_gather_fp8, veda_attend_fp8, veda_quantize_int8, veda_gather_int8, veda_attend_int8,
     veda_layout_export_direct, veda_pool, veda_attend_direct,
+    veda_teacher, veda_bias_buckets, veda_bias_index, veda_score_bias_workspace_bytes, veda_score_bias,
+    veda_bias_backward_workspace_bytes, veda_bias_backward, veda_distill, veda_score_backward_workspace_bytes,
+    veda_score_backward,
 )
 from .layer import VedaLayer  # noqa: F401
 from .pipeline import HostPipeline  # noqa: F401

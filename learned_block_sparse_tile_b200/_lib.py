@@ -7,6 +7,7 @@ library is missing or the device is not an sm_100 part, calls raise instead of f
 from __future__ import annotations
 
 import ctypes as C
+import functools
 import os
 
 import numpy as np
@@ -26,6 +27,9 @@ EXPORTS = [
     "veda_attend_direct", "veda_debug_exp2", "veda_grid_of", "veda_describe_packed_layout",
     "veda_attend_paired_workspace_bytes", "veda_attend_paired", "veda_attend_direct_paired", "veda_debug_attend_ctas",
     "veda_attend_fp8_paired", "veda_attend_int8_paired",
+    "veda_teacher", "veda_bias_buckets", "veda_bias_index", "veda_score_bias_workspace_bytes", "veda_score_bias",
+    "veda_bias_backward_workspace_bytes", "veda_bias_backward", "veda_distill", "veda_score_backward_workspace_bytes",
+    "veda_score_backward",
 ]
 
 VEDA_SEG_OTHER, VEDA_SEG_VIDEO, VEDA_SEG_COND, VEDA_SEG_REF_IMG = range(4)
@@ -58,6 +62,10 @@ class PackedDesc(C.Structure):
 
 class Budget(C.Structure):
     _fields_ = [("kind", C.c_int32), ("ratio", C.c_double), ("tiles", C.c_int64)]
+
+
+class BiasSpec(C.Structure):
+    _fields_ = [("reach", C.c_int32 * 3), ("far_tiles", C.c_int32 * 3)]
 
 
 class BlockDesc(C.Structure):
@@ -131,6 +139,19 @@ def lib():
         L.veda_grid_of.argtypes = [p, i64, i64, C.POINTER(C.c_int32), C.POINTER(C.c_int32)]
         L.veda_describe_packed_layout.argtypes = [C.POINTER(Segment), i32, i64, C.POINTER(C.c_int32), p,
                                                   C.POINTER(PackedDesc)]
+        spec = C.POINTER(BiasSpec)
+        L.veda_teacher.argtypes = [vp, p, p, i32, i32, p, p, vp]
+        L.veda_bias_buckets.argtypes = [spec, C.POINTER(C.c_int32)]
+        L.veda_bias_index.argtypes = [vp, spec, p]
+        L.veda_score_bias_workspace_bytes.argtypes = [vp, i32, i32]
+        L.veda_score_bias.argtypes = [vp, p, p, i32, i32, p, p, spec, p, p, p, C.c_size_t, p, vp]
+        L.veda_bias_backward_workspace_bytes.argtypes = [vp, i32, spec]
+        L.veda_bias_backward.argtypes = [vp, p, i32, spec, p, C.c_size_t, p, vp]
+        L.veda_distill.argtypes = [vp, p, i32, p, p, p, i32, i32, C.c_float, p, p, p, vp]
+        L.veda_score_backward_workspace_bytes.argtypes = [vp, i32, i32]
+        L.veda_score_backward.argtypes = [vp, p, p, i32, i32, p, p, p, p, p, C.c_size_t, vp]
+        for name in ("veda_score_bias", "veda_bias_backward", "veda_score_backward"):
+            getattr(L, name + "_workspace_bytes").restype = C.c_size_t
         _lib = L
     return _lib
 
@@ -379,6 +400,148 @@ def veda_attend_int8_paired(layout, q_codes, k_codes, scales_q, scales_k, v_t, k
     """veda_attend_int8 two neighbouring query tiles at a time (as veda_attend_fp8_paired)."""
     _attend_codes_paired(lib().veda_attend_int8_paired, layout, q_codes, k_codes, scales_q, scales_k, v_t, kept_idx,
                          kept_cnt, out, heads, q_row_sq, k_max_sq, workspace, stream)
+
+
+def _need(who, device, *tensors):
+    """Refuses tensors a kernel would misread: each (name, tensor, dtype, shape) must be a contiguous CUDA tensor of
+    that type and shape, all of them on the current device (``device``: its index)."""
+    for name, t, dtype, shape in tensors:
+        if t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
+            raise VedaError(VEDA_ERR_INVALID, f"{who}: {name} must be contiguous {dtype} of shape {tuple(shape)}, not "
+                            f"{t.dtype} of shape {tuple(t.shape)} with strides {t.stride()}")
+        if t.get_device() != device:
+            raise VedaError(VEDA_ERR_INVALID, f"{who}: {name} is on {t.device}, the current device is cuda:{device}")
+
+
+def _workspace(who, device, t):
+    if not t.is_contiguous() or t.get_device() != device:
+        raise VedaError(VEDA_ERR_INVALID, f"{who}: the workspace must be contiguous on the current device")
+    return _ptr(t), t.numel() * t.element_size()
+
+
+@functools.lru_cache(maxsize=256)
+def _bias_spec(reach, far):
+    """(the C specification, its number of buckets) of per-axis (t, h, w) reaches and far distances."""
+    spec = BiasSpec((C.c_int32 * 3)(*reach), (C.c_int32 * 3)(*far))
+    n = C.c_int32()
+    _check(lib().veda_bias_buckets(C.byref(spec), C.byref(n)))
+    return spec, n.value
+
+
+def _spec_bytes(reach):
+    """A specification of these reaches for the size queries, which do not depend on the distances."""
+    return C.byref(_bias_spec(tuple(reach), (32767, 32767, 32767))[0])
+
+
+def veda_teacher(layout, q_t, k_t, teacher, row_lse=None, stream=None):
+    """q_t/k_t: bf16 [n, N, D] tile order; teacher: fp32 [n, n_video, n_video] out; row_lse: fp32 [n, S] or None."""
+    import torch
+    dev, shape = torch.cuda.current_device(), q_t.shape
+    if len(shape) != 3:
+        raise VedaError(VEDA_ERR_INVALID, "veda_teacher: q_t must be [n, N, D]")
+    n, nv = shape[0], layout.n_video
+    want = (n, layout.n_slots, shape[2])
+    _need("veda_teacher", dev, ("q_t", q_t, torch.bfloat16, want), ("k_t", k_t, torch.bfloat16, want),
+          ("teacher", teacher, torch.float32, (n, nv, nv)))
+    if row_lse is not None:
+        _need("veda_teacher", dev, ("row_lse", row_lse, torch.float32, (n, layout.seq_len)))
+    _check(lib().veda_teacher(layout.handle, _ptr(q_t), _ptr(k_t), n, shape[2], _ptr(row_lse), _ptr(teacher),
+                              _stream(stream)))
+
+
+def veda_bias_buckets(reach, far):
+    """Number of buckets of the relative position bias: per-axis (t, h, w) reaches and far distances in tiles."""
+    return _bias_spec(tuple(reach), tuple(far))[1]
+
+
+def veda_bias_index(layout, reach, far):
+    """The bucket of every (query tile, key tile) pair, an int32 numpy array [n_video, n_video]."""
+    spec, _ = _bias_spec(tuple(reach), tuple(far))
+    out = np.empty((layout.n_video, layout.n_video), np.int32)
+    _check(lib().veda_bias_index(layout.handle, C.byref(spec), out.ctypes.data))
+    return out
+
+
+def veda_score_bias_workspace_bytes(layout, n_heads, dim, reach=None):
+    """Bytes of workspace veda_score_bias needs (``reach`` does not change it)."""
+    return int(lib().veda_score_bias_workspace_bytes(layout.handle, n_heads, dim))
+
+
+def veda_score_bias(layout, feats_q, feats_k, proj_q, proj_k, reach, far, bias, hats, workspace, scores, stream=None):
+    """veda_score with a bias per bucket: bias fp32 [n, buckets] (reach, far and bias None: no bias); hats: fp32
+    [2, n, n_video, D] out, kept for veda_score_backward; scores: fp32 [n, n_video, n_video] out."""
+    import torch
+    dev, f32 = torch.cuda.current_device(), torch.float32
+    if len(proj_q.shape) != 3:
+        raise VedaError(VEDA_ERR_INVALID, "veda_score_bias: proj_q must be [n, 3D, D]")
+    n, _, dim = proj_q.shape
+    nv = layout.n_video
+    _need("veda_score_bias", dev, ("feats_q", feats_q, f32, (n, nv, 3 * dim)), ("feats_k", feats_k, f32, (n, nv, 3 * dim)),
+          ("proj_q", proj_q, f32, (n, 3 * dim, dim)), ("proj_k", proj_k, f32, (n, 3 * dim, dim)),
+          ("hats", hats, f32, (2, n, nv, dim)), ("scores", scores, f32, (n, nv, nv)))
+    spec = None
+    if bias is not None:
+        spec, buckets = _bias_spec(tuple(reach), tuple(far))
+        _need("veda_score_bias", dev, ("bias", bias, f32, (n, buckets)))
+    _check(lib().veda_score_bias(layout.handle, _ptr(feats_q), _ptr(feats_k), n, dim, _ptr(proj_q), _ptr(proj_k),
+                                 None if spec is None else C.byref(spec), _ptr(bias), _ptr(hats),
+                                 *_workspace("veda_score_bias", dev, workspace), _ptr(scores), _stream(stream)))
+
+
+def veda_bias_backward_workspace_bytes(layout, n_heads, reach):
+    return int(lib().veda_bias_backward_workspace_bytes(layout.handle, n_heads, _spec_bytes(reach)))
+
+
+def veda_bias_backward(layout, d_scores, reach, far, workspace, d_bias, stream=None):
+    """d_scores: fp32 [n, n_video, n_video]; d_bias: fp32 [n, buckets] out."""
+    import torch
+    dev, n, nv = torch.cuda.current_device(), d_scores.shape[0], layout.n_video
+    spec, buckets = _bias_spec(tuple(reach), tuple(far))
+    _need("veda_bias_backward", dev, ("d_scores", d_scores, torch.float32, (n, nv, nv)),
+          ("d_bias", d_bias, torch.float32, (n, buckets)))
+    _check(lib().veda_bias_backward(layout.handle, _ptr(d_scores), n, C.byref(spec),
+                                    *_workspace("veda_bias_backward", dev, workspace), _ptr(d_bias), _stream(stream)))
+
+
+def veda_distill(layout, scores, t_idx, t_val, t_cnt, tau, loss, d_scores=None, row_weight=None, by_column=False,
+                 stream=None):
+    """scores: fp32 [n, n_video, n_video]; t_idx: int32 [n, n_video, width] and t_cnt: int32 [n, n_video] (veda_select's
+    lists); t_val: fp32 [n, n_video, width], or [n, n_video, n_video] with by_column; loss: fp32 [n, n_video] out;
+    d_scores: fp32 like scores, out, or None; row_weight: fp32 [n, n_video] or None."""
+    import torch
+    dev, f32, n, nv = torch.cuda.current_device(), torch.float32, scores.shape[0], layout.n_video
+    width = t_idx.shape[-1]
+    _need("veda_distill", dev, ("scores", scores, f32, (n, nv, nv)), ("t_idx", t_idx, torch.int32, (n, nv, width)),
+          ("t_val", t_val, f32, (n, nv, nv if by_column else width)), ("t_cnt", t_cnt, torch.int32, (n, nv)),
+          ("loss", loss, f32, (n, nv)))
+    if d_scores is not None:
+        _need("veda_distill", dev, ("d_scores", d_scores, f32, (n, nv, nv)))
+    if row_weight is not None:
+        _need("veda_distill", dev, ("row_weight", row_weight, f32, (n, nv)))
+    _check(lib().veda_distill(layout.handle, _ptr(scores), n, _ptr(t_idx), _ptr(t_val), _ptr(t_cnt), width,
+                              int(by_column), float(tau), _ptr(row_weight), _ptr(loss), _ptr(d_scores),
+                              _stream(stream)))
+
+
+def veda_score_backward_workspace_bytes(layout, n_heads, dim):
+    return int(lib().veda_score_backward_workspace_bytes(layout.handle, n_heads, dim))
+
+
+def veda_score_backward(layout, feats_q, feats_k, hats, d_scores, workspace, d_proj_q, d_proj_k, stream=None):
+    """hats: fp32 [2, n, n_video, D] from veda_score_bias; d_scores: fp32 [n, n_video, n_video]; d_proj_q / d_proj_k:
+    fp32 [n, 3D, D] out."""
+    import torch
+    dev, f32 = torch.cuda.current_device(), torch.float32
+    if len(hats.shape) != 4:
+        raise VedaError(VEDA_ERR_INVALID, "veda_score_backward: hats must be [2, n, n_video, D]")
+    n, dim, nv = hats.shape[1], hats.shape[3], layout.n_video
+    _need("veda_score_backward", dev, ("feats_q", feats_q, f32, (n, nv, 3 * dim)),
+          ("feats_k", feats_k, f32, (n, nv, 3 * dim)), ("hats", hats, f32, (2, n, nv, dim)),
+          ("d_scores", d_scores, f32, (n, nv, nv)), ("d_proj_q", d_proj_q, f32, (n, 3 * dim, dim)),
+          ("d_proj_k", d_proj_k, f32, (n, 3 * dim, dim)))
+    ws, size = _workspace("veda_score_backward", dev, workspace)
+    _check(lib().veda_score_backward(layout.handle, _ptr(feats_q), _ptr(feats_k), n, dim, _ptr(hats), _ptr(d_scores),
+                                     _ptr(d_proj_q), _ptr(d_proj_k), ws, size, _stream(stream)))
 
 
 def veda_sync_status(stream=None):

@@ -9,9 +9,9 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libveda.so")
 
-SOURCES = ["veda_api.cu", "veda_plan.cpp", "veda_score_noalloc.cu"]
+SOURCES = ["veda_api.cu", "veda_plan.cpp", "veda_score_noalloc.cu", "veda_train.cu"]
 HEADERS = ["veda_internal.h", "ptx.cuh", "gather.cuh", "score.cuh", "select.cuh", "attend.cuh", "attend_pair.cuh",
-           "quant.cuh"]
+           "quant.cuh", "bias.cuh", "distill.cuh", "train_gemm.cuh"]
 
 
 def nvcc_path():
@@ -22,7 +22,7 @@ def nvcc_path():
 
 
 def command(out=LIB, extra=()):
-    return [nvcc_path(), "-O3", "-std=c++17", "-shared", "-Xcompiler", "-fPIC,-ffp-contract=off",
+    return [nvcc_path(), "--threads", "0", "-O3", "-std=c++17", "-shared", "-Xcompiler", "-fPIC,-ffp-contract=off",
             "-gencode", "arch=compute_100a,code=sm_100a", "-lineinfo", "--expt-relaxed-constexpr",
             "-I", os.path.join(ROOT, "include"), "-I", CSRC, *extra,
             "-o", out] + [os.path.join(CSRC, s) for s in SOURCES]

@@ -1,0 +1,156 @@
+// Learned relative position bias of the tile scores, by buckets of the two tiles' offset.
+//
+// A video tile has a place (t, h, w) in its span's array of tiles. Two tiles of one span have the offset
+// r = key place - query place, and per axis the distance |r| falls into one of `reach` classes: the first
+// e = (reach + 1) / 2 hold one distance each, the others widen geometrically up to `far` tiles (class
+// e + m starts at the smallest a with a^k >= e^(k - m) far^m, k = reach - e; whole numbers, so nothing
+// rounds at a border). With the sign of r an axis has 2 reach - 1 indices, and the pair's bucket is the
+// three axes' mixed-radix number. Pairs of tiles of different spans share two more buckets: the key's
+// span before, and behind, the query's.
+#pragma once
+
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+namespace veda {
+
+constexpr int kBiasMaxReach = 16;
+constexpr int kBiasMaxBuckets = 4096;
+
+// starts[a][c] = the smallest distance of class c (c >= 1) on axis a
+struct BiasClasses {
+    int reach[3];
+    int starts[3][kBiasMaxReach];
+    int buckets;  // all of them, the two of other spans last
+};
+
+// index of a signed offset on one axis: 0 .. 2 reach - 2
+__host__ __device__ __forceinline__ int bias_axis_index(const int* starts, int reach, int r) {
+    const int a = r < 0 ? -r : r;
+    int c = 0;
+    for (int k = 1; k < reach; ++k) c += a >= starts[k];
+    return r > 0 ? reach - 1 + c : c;
+}
+
+__host__ __device__ __forceinline__ int bias_bucket(const BiasClasses& b, int dt, int dh, int dw) {
+    const int it = bias_axis_index(b.starts[0], b.reach[0], dt);
+    const int ih = bias_axis_index(b.starts[1], b.reach[1], dh);
+    const int iw = bias_axis_index(b.starts[2], b.reach[2], dw);
+    return (it * (2 * b.reach[1] - 1) + ih) * (2 * b.reach[2] - 1) + iw;
+}
+
+// Offsets as one number. In a span of T x H x W tiles a place's number is (t (2H - 1) + h) (2W - 1) + w, and an
+// offset's number is the difference of two places' numbers, so the bias of a pair is one load of a table per
+// head that holds the bias of every offset: the spans' offsets one span after the other ((2T - 1)(2H - 1)(2W - 1)
+// each, fewer than 8 per tile), then the two buckets of other spans. The layout keeps each tile's part of the
+// index as a key (its number) and as a query (where the table's part of its span is centred, less its number).
+
+// table[head][o] = bias[head][bucket(o)]
+__global__ void __launch_bounds__(256) bias_expand_kernel(const float* bias, float* table, BiasClasses b,
+                                                          const int4* span_grid, int n_spans, int count) {
+    const int i = blockIdx.x * 256 + threadIdx.x;
+    if (i >= count + 2) return;
+    int bucket = b.buckets - 2 + (i - count);
+    if (i < count) {
+        int o = i;
+        int4 g = span_grid[0];
+        for (int s = 0; s < n_spans; ++s) {
+            g = span_grid[s];
+            const int offsets = (2 * g.y - 1) * (2 * g.z - 1) * (2 * g.w - 1);
+            if (o < offsets) break;
+            o -= offsets;
+        }
+        const int rh = 2 * g.z - 1, rw = 2 * g.w - 1;
+        bucket = bias_bucket(b, o / (rw * rh) - (g.y - 1), (o / rw) % rh - (g.z - 1), o % rw - (g.w - 1));
+    }
+    table[int64_t(blockIdx.y) * (count + 2) + i] = bias[int64_t(blockIdx.y) * b.buckets + bucket];
+}
+
+struct BiasBackwardArgs {
+    const float* d_scores;     // [n_heads, n, n]
+    const int4* tile_pos;      // [n] {span, t, h, w}
+    const int4* span_grid;     // [n_spans] {first tile, tiles along t, h, w}
+    float* partial;            // [n_heads, chunks, buckets]
+    int n, rows_per_chunk;
+    BiasClasses b;
+};
+
+// places [lo, hi) of an axis of `count` places whose offset from `at` has index `idx`
+__device__ __forceinline__ void bias_interval(const int* starts, int reach, int idx, int at, int count, int& lo, int& hi) {
+    if (reach == 1) {
+        lo = 0;
+        hi = count;
+        return;
+    }
+    const int c = idx < reach ? idx : idx - reach + 1;
+    const int a0 = c == 0 ? 0 : starts[c], a1 = c + 1 < reach ? starts[c + 1] - 1 : 1 << 28;
+    if (idx < reach && c > 0) {  // r = -a1 .. -a0
+        lo = at - a1;
+        hi = at - a0 + 1;
+    } else if (idx < reach) {    // r = 0
+        lo = at - a1;
+        hi = at + 1;
+    } else {                     // r = a0 .. a1
+        lo = at + a0;
+        hi = at + a1 + 1;
+    }
+    lo = max(lo, 0);
+    hi = min(hi, count);
+}
+
+// Sums of one chunk of query rows: each bucket of a row is a box of its span's tile array (the classes are
+// intervals of the offset), and a thread adds its buckets' boxes in a fixed order, so nothing is atomic.
+__global__ void __launch_bounds__(256) bias_backward_kernel(const BiasBackwardArgs a) {
+    extern __shared__ float row[];
+    const int head = blockIdx.y, pairs = a.b.buckets - 2;
+    const int i0 = blockIdx.x * a.rows_per_chunk, i1 = min(a.n, i0 + a.rows_per_chunk);
+    const int nh = 2 * a.b.reach[1] - 1, nw = 2 * a.b.reach[2] - 1;
+    float* out = a.partial + (int64_t(head) * gridDim.x + blockIdx.x) * a.b.buckets;
+    float acc[kBiasMaxBuckets / 256] = {};
+    for (int i = i0; i < i1; ++i) {
+        const float* src = a.d_scores + (int64_t(head) * a.n + i) * a.n;
+        __syncthreads();
+        for (int j = threadIdx.x; j < a.n; j += 256) row[j] = src[j];
+        __syncthreads();
+        const int4 p = a.tile_pos[i];
+        const int4 g = a.span_grid[p.x];
+        const int end = g.x + g.y * g.z * g.w;
+#pragma unroll
+        for (int u = 0; u < kBiasMaxBuckets / 256; ++u) {
+            const int b = threadIdx.x + 256 * u;
+            if (b >= a.b.buckets) break;
+            float sum = 0.f;
+            if (b >= pairs) {
+                const int lo = b == pairs ? 0 : end, hi = b == pairs ? g.x : a.n;
+                for (int j = lo; j < hi; ++j) sum += row[j];
+            } else {
+                int t0, t1, h0, h1, w0, w1;
+                bias_interval(a.b.starts[0], a.b.reach[0], b / (nw * nh), p.y, g.y, t0, t1);
+                bias_interval(a.b.starts[1], a.b.reach[1], (b / nw) % nh, p.z, g.z, h0, h1);
+                bias_interval(a.b.starts[2], a.b.reach[2], b % nw, p.w, g.w, w0, w1);
+                for (int h = h0; h < h1; ++h)
+                    for (int w = w0; w < w1; ++w)
+                        for (int t = t0; t < t1; ++t) sum += row[g.x + (h * g.w + w) * g.y + t];
+            }
+            acc[u] += sum;
+        }
+    }
+#pragma unroll
+    for (int u = 0; u < kBiasMaxBuckets / 256; ++u) {
+        const int b = threadIdx.x + 256 * u;
+        if (b < a.b.buckets) out[b] = acc[u];
+    }
+}
+
+// d_bias[head][b] = the chunks' sums, added in chunk order
+__global__ void __launch_bounds__(256) bias_reduce_kernel(const float* partial, float* d_bias, int chunks, int buckets) {
+    const int b = blockIdx.x * 256 + threadIdx.x;
+    if (b >= buckets) return;
+    const float* p = partial + int64_t(blockIdx.y) * chunks * buckets + b;
+    float sum = 0.f;
+    for (int c = 0; c < chunks; ++c) sum += p[int64_t(c) * buckets];
+    d_bias[int64_t(blockIdx.y) * buckets + b] = sum;
+}
+
+}  // namespace veda

@@ -89,7 +89,8 @@ int device_copy(const veda_layout* lay, const DeviceCopy** out) {
         if ((e = up(&dc.perm, lay->perm)) != cudaSuccess || (e = up(&dc.valid_count, lay->valid_count)) != cudaSuccess ||
             (e = up(&dc.ok_list, lay->ok_list)) != cudaSuccess || (e = up(&dc.allowed, lay->allowed)) != cudaSuccess ||
             (e = up(&dc.box_perm, lay->box_perm)) != cudaSuccess || (e = up(&dc.tile_coord, lay->tile_coord)) != cudaSuccess ||
-            (e = up(&dc.tile_mask, lay->tile_mask)) != cudaSuccess)
+            (e = up(&dc.tile_mask, lay->tile_mask)) != cudaSuccess || (e = up(&dc.tile_pos, lay->tile_pos)) != cudaSuccess ||
+            (e = up(&dc.tile_num, lay->tile_num)) != cudaSuccess || (e = up(&dc.span_grid, lay->span_grid)) != cudaSuccess)
             return cuda_fail(e, "uploading the layout");
         dc.ready = true;
     }
@@ -152,6 +153,19 @@ int fail(int code, const std::string& msg) {
 }
 
 void clear_error() { t_error.clear(); }
+
+int current_device(DeviceInfo* out) {
+    DeviceState* ds;
+    if (int rc = device_state(&ds)) return rc;
+    cudaError_t e = cudaGetDevice(&out->ordinal);
+    if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
+    out->sms = ds->sms;
+    out->err = ds->err;
+    return VEDA_OK;
+}
+int layout_on_device(const veda_layout* lay, const DeviceCopy** out) { return device_copy(lay, out); }
+uint64_t wait_timeout_ns() { return g_timeout_ns.load(); }
+int launch_status(const char* what) { return launch_check(what); }
 
 }  // namespace veda
 
@@ -220,6 +234,9 @@ extern "C" void veda_layout_destroy(veda_layout* layout) {
             cudaFree(dc.box_perm);
             cudaFree(dc.tile_coord);
             cudaFree(dc.tile_mask);
+            cudaFree(dc.tile_pos);
+            cudaFree(dc.tile_num);
+            cudaFree(dc.span_grid);
         }
     }
     if (have) cudaSetDevice(cur);

@@ -33,11 +33,27 @@ struct DeviceCopy {
     int32_t* box_perm = nullptr;     // [n_slots] (gather-free attend)
     int32_t* tile_coord = nullptr;   // [n_tiles * 4]
     int32_t* tile_mask = nullptr;    // [n_tiles * 4] (bit patterns)
+    int32_t* tile_pos = nullptr;     // [n_video * 4]
+    int32_t* tile_num = nullptr;     // [n_video * 4]
+    int32_t* span_grid = nullptr;    // [n_spans * 4]
 };
 
 // Records `msg` as the calling thread's last error and returns `code`.
 int fail(int code, const std::string& msg);
 void clear_error();
+
+// The current device, as the entry points outside veda_api.cu need it.
+struct DeviceInfo {
+    int ordinal = 0;
+    int sms = 0;
+    int* err = nullptr;  // device address of the latched error bits
+};
+int current_device(DeviceInfo* out);
+// Device copy of a layout's index data on the current device (made on first use).
+int layout_on_device(const veda_layout* lay, const DeviceCopy** out);
+uint64_t wait_timeout_ns();
+// `cudaGetLastError` after a launch, as a VEDA_* status
+int launch_status(const char* what);
 
 // Floats of scratch the predictor's products need per head: the projected q and k features (2 n_video D)
 // and the two projections transposed (2 x 3D x D).
@@ -66,6 +82,14 @@ struct veda_layout {
     std::vector<int32_t> tile_coord;  // [n_tiles * 4] span tile {span, w0, h0, t0}; global tile {-1, row0, 0, 0}
     std::vector<int32_t> tile_mask;   // [n_tiles * 4] bit c (word c / 32) set: box position c holds a row
     std::vector<veda::DirectSpan> spans;  // tiled spans, in tile order
+    // The tiled spans' tiles as 3D arrays, for the relative position bias: span {first tile, tiles along t, h,
+    // w}; video tile {span, t, h, w} (its box's place in its span's array)
+    std::vector<int32_t> span_grid;   // [n_spans * 4]
+    std::vector<int32_t> tile_pos;    // [n_video * 4]
+    // video tile {span, its number as a key, its number as a query, 0}: key number + query number of two tiles
+    // of one span is their offset's place among the bias_offsets offsets of all spans (bias.cuh)
+    std::vector<int32_t> tile_num;    // [n_video * 4]
+    int32_t bias_offsets = 0;
     bool direct_ok = false;           // every global tile's rows are consecutive; spans <= kMaxDirectSpans
     std::string direct_why;           // why not, when direct_ok is false
     mutable std::mutex mu;

@@ -1,0 +1,316 @@
+// C ABI entry points that train the tile predictor: the pooled teacher, the scores with a relative position
+// bias, the distillation loss and the gradients. Argument checks and launches; the kernels live in
+// teacher.cuh, train_gemm.cuh, bias.cuh and distill.cuh.
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+#include <cstring>
+#include <string>
+
+#include "veda_internal.h"
+#include "bias.cuh"
+#include "distill.cuh"
+#include "train_gemm.cuh"
+
+using namespace veda;
+
+namespace {
+
+constexpr int kMaxTrainTiles = 16384;  // the widest row veda_select takes
+
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+size_t round256(size_t b) { return (b + 255) & ~size_t(255); }
+
+template <class F>
+int guarded(F&& f) {
+    try {
+        return f();
+    } catch (...) {
+        return VEDA_ERR_CUDA;  // out of host memory while a message was made
+    }
+}
+
+int check_heads(const char* who, int32_t n_heads, int32_t dim) {
+    if (dim != 64 && dim != 128) return fail(VEDA_ERR_INVALID, std::string(who) + ": head_dim must be 64 or 128");
+    if (n_heads <= 0) return fail(VEDA_ERR_INVALID, std::string(who) + ": n_heads must be positive");
+    return VEDA_OK;
+}
+
+int check_size(const char* who, const veda_layout* layout, int32_t n_heads) {
+    if (layout->desc.n_video > kMaxTrainTiles || n_heads > 65535)
+        return fail(VEDA_ERR_UNSUPPORTED, std::string(who) + ": at most 16384 video tiles and 65535 heads");
+    return VEDA_OK;
+}
+
+int classes_of(const char* who, const veda_bias_spec* spec, BiasClasses* out) {
+    if (!spec) return fail(VEDA_ERR_INVALID, std::string(who) + ": the bias specification is NULL");
+    int64_t buckets = 1;
+    for (int a = 0; a < 3; ++a) {
+        const int reach = spec->reach[a], far = spec->far_tiles[a], exact = (reach + 1) / 2, wide = reach - exact;
+        if (reach < 1 || reach > kBiasMaxReach)
+            return fail(VEDA_ERR_INVALID, std::string(who) + ": reach must lie in [1, 16] on every axis");
+        if (far <= exact || far > 32767)
+            return fail(VEDA_ERR_INVALID, std::string(who) + ": far must lie in ((reach + 1) / 2, 32767] on every axis");
+        out->reach[a] = reach;
+        for (int c = 0; c < kBiasMaxReach; ++c) out->starts[a][c] = c;
+        for (int m = 1; exact + m < reach; ++m) {
+            unsigned __int128 bound = 1;  // exact^(wide - m) far^m < 2^120
+            for (int k = 0; k < wide; ++k) bound *= unsigned(k < m ? far : exact);
+            int lo = exact, hi = far;     // the smallest distance whose wide-th power reaches the bound
+            while (lo < hi) {
+                const int mid = (lo + hi) / 2;
+                unsigned __int128 p = 1;
+                for (int k = 0; k < wide; ++k) p *= unsigned(mid);
+                if (p >= bound) hi = mid; else lo = mid + 1;
+            }
+            out->starts[a][exact + m] = lo;
+        }
+        buckets *= 2 * reach - 1;
+    }
+    buckets += 2;
+    if (buckets > kBiasMaxBuckets)
+        return fail(VEDA_ERR_UNSUPPORTED, std::string(who) + ": at most 4096 buckets");
+    out->buckets = int(buckets);
+    return VEDA_OK;
+}
+
+// query rows of one chunk of the bias gradient's sums: enough chunks to fill the GPU, few enough to add up
+int bias_chunk_rows(int n) { return std::max(1, (n + 31) / 32); }
+int bias_chunks(int n) { return (n + bias_chunk_rows(n) - 1) / bias_chunk_rows(n); }
+
+}  // namespace
+
+extern "C" int veda_bias_buckets(const veda_bias_spec* spec, int32_t* n_buckets) {
+    return guarded([&] {
+        clear_error();
+        if (!n_buckets) return fail(VEDA_ERR_INVALID, "veda_bias_buckets: NULL argument");
+        BiasClasses b;
+        if (int rc = classes_of("veda_bias_buckets", spec, &b)) return rc;
+        *n_buckets = b.buckets;
+        return VEDA_OK;
+    });
+}
+
+extern "C" int veda_bias_index(const veda_layout* layout, const veda_bias_spec* spec, int32_t* index) {
+    return guarded([&] {
+        clear_error();
+        if (!layout || !index) return fail(VEDA_ERR_INVALID, "veda_bias_index: NULL argument");
+        BiasClasses b;
+        if (int rc = classes_of("veda_bias_index", spec, &b)) return rc;
+        const int64_t n = layout->desc.n_video;
+        const int32_t* pos = layout->tile_pos.data();
+        for (int64_t i = 0; i < n; ++i)
+            for (int64_t j = 0; j < n; ++j) {
+                const int32_t *q = pos + 4 * i, *k = pos + 4 * j;
+                index[i * n + j] = k[0] < q[0]   ? b.buckets - 2
+                                   : k[0] > q[0] ? b.buckets - 1
+                                                 : bias_bucket(b, k[1] - q[1], k[2] - q[2], k[3] - q[3]);
+            }
+        return VEDA_OK;
+    });
+}
+
+extern "C" int veda_teacher(const veda_layout* layout, const void* q_t, const void* k_t, int32_t n_heads, int32_t dim,
+                            const float* row_lse, float* teacher, void* stream) {
+    return guarded([&] {
+        clear_error();
+        if (!layout || !q_t || !k_t || !teacher) return fail(VEDA_ERR_INVALID, "veda_teacher: NULL argument");
+        if (int rc = check_heads("veda_teacher", n_heads, dim)) return rc;
+        if (!aligned16(q_t) || !aligned16(k_t) || !aligned16(row_lse) || !aligned16(teacher))
+            return fail(VEDA_ERR_INVALID, "veda_teacher: buffers need 16-byte alignment");
+        if (int rc = check_size("veda_teacher", layout, n_heads)) return rc;
+        DeviceInfo di;
+        if (int rc = current_device(&di)) return rc;
+        const DeviceCopy* dc;
+        if (int rc = layout_on_device(layout, &dc)) return rc;
+        const veda_layout_desc& d = layout->desc;
+        const int n = d.n_video;
+        train::Operand<__nv_bfloat16> A{static_cast<const __nv_bfloat16*>(q_t), d.n_slots * dim, dim, 1, n * kTile};
+        train::Operand<__nv_bfloat16> B = A;
+        B.base = static_cast<const __nv_bfloat16*>(k_t);
+        train::PoolEpilogue e{teacher, n, float(1.0 / std::sqrt(double(dim))), dc->valid_count, dc->perm, row_lse, d.seq_len};
+        train::gemm_kernel<<<dim3(n, n, n_heads), 256, 0, static_cast<cudaStream_t>(stream)>>>(A, B, dim, e);
+        return launch_status("teacher gemm_kernel");
+    });
+}
+
+extern "C" size_t veda_score_bias_workspace_bytes(const veda_layout* layout, int32_t n_heads, int32_t dim) {
+    if (!layout || n_heads <= 0 || dim <= 0) return 0;
+    return round256(size_t(n_heads) * size_t(layout->bias_offsets + 2) * sizeof(float));
+}
+
+extern "C" int veda_score_bias(const veda_layout* layout, const float* feats_q, const float* feats_k, int32_t n_heads,
+                               int32_t dim, const float* proj_q, const float* proj_k, const veda_bias_spec* spec,
+                               const float* bias, float* hats, void* workspace, size_t workspace_bytes, float* scores,
+                               void* stream) {
+    return guarded([&] {
+        clear_error();
+        if (!layout || !feats_q || !feats_k || !proj_q || !proj_k || !hats || !workspace || !scores || !spec != !bias)
+            return fail(VEDA_ERR_INVALID, "veda_score_bias: NULL argument (spec and bias go together)");
+        if (int rc = check_heads("veda_score_bias", n_heads, dim)) return rc;
+        if (workspace_bytes < veda_score_bias_workspace_bytes(layout, n_heads, dim))
+            return fail(VEDA_ERR_INVALID, "veda_score_bias: workspace smaller than veda_score_bias_workspace_bytes()");
+        for (const void* p : {(const void*)feats_q, (const void*)feats_k, (const void*)proj_q, (const void*)proj_k,
+                              (const void*)bias, (const void*)hats, (const void*)workspace, (const void*)scores})
+            if (!aligned16(p)) return fail(VEDA_ERR_INVALID, "veda_score_bias: buffers need 16-byte alignment");
+        if (int rc = check_size("veda_score_bias", layout, n_heads)) return rc;
+        BiasClasses b;
+        if (spec)
+            if (int rc = classes_of("veda_score_bias", spec, &b)) return rc;
+        DeviceInfo di;
+        if (int rc = current_device(&di)) return rc;
+        const DeviceCopy* dc;
+        if (int rc = layout_on_device(layout, &dc)) return rc;
+        const int n = layout->desc.n_video;
+        const int offsets = layout->bias_offsets;
+        cudaStream_t s = static_cast<cudaStream_t>(stream);
+        float* table = static_cast<float*>(workspace);
+        if (bias) {
+            bias_expand_kernel<<<dim3((offsets + 2 + 255) / 256, n_heads), 256, 0, s>>>(
+                bias, table, b, reinterpret_cast<const int4*>(dc->span_grid), int(layout->span_grid.size() / 4), offsets);
+            if (int rc = launch_status("bias_expand_kernel")) return rc;
+        }
+        const int64_t nf = int64_t(n) * 3 * dim, nd = int64_t(n) * dim;
+        for (int side = 0; side < 2; ++side) {
+            const float* f = side ? feats_k : feats_q;
+            train::Operand<float> A{f, nf, 3 * dim, 1, n};
+            train::Operand<float> B{side ? proj_k : proj_q, 3 * int64_t(dim) * dim, 1, dim, dim};
+            train::StoreEpilogue e{hats + side * n_heads * nd, nd, n, dim, 1.f, f, nf, 3 * dim};
+            train::gemm_kernel<<<dim3(1, (n + 127) / 128, n_heads), 256, 0, s>>>(A, B, 3 * dim, e);
+            if (int rc = launch_status("score_bias gemm_kernel (projections)")) return rc;
+        }
+        train::Operand<float> A{hats, nd, dim, 1, n}, B{hats + n_heads * nd, nd, dim, 1, n};
+        train::BiasEpilogue e{scores, n, float(1.0 / std::sqrt(double(dim))), bias ? table : nullptr, offsets + 2,
+                              reinterpret_cast<const int4*>(dc->tile_num), offsets};
+        train::gemm_kernel<<<dim3((n + 127) / 128, (n + 127) / 128, n_heads), 256, 0, s>>>(A, B, dim, e);
+        return launch_status("score_bias gemm_kernel (logits)");
+    });
+}
+
+extern "C" size_t veda_bias_backward_workspace_bytes(const veda_layout* layout, int32_t n_heads, const veda_bias_spec* spec) {
+    BiasClasses b;
+    if (!layout || n_heads <= 0 || guarded([&] { return classes_of("veda_bias_backward_workspace_bytes", spec, &b); })) return 0;
+    return round256(size_t(n_heads) * bias_chunks(layout->desc.n_video) * size_t(b.buckets) * sizeof(float));
+}
+
+extern "C" int veda_bias_backward(const veda_layout* layout, const float* d_scores, int32_t n_heads,
+                                  const veda_bias_spec* spec, void* workspace, size_t workspace_bytes, float* d_bias,
+                                  void* stream) {
+    return guarded([&] {
+        clear_error();
+        if (!layout || !d_scores || !workspace || !d_bias) return fail(VEDA_ERR_INVALID, "veda_bias_backward: NULL argument");
+        if (n_heads <= 0) return fail(VEDA_ERR_INVALID, "veda_bias_backward: n_heads must be positive");
+        BiasBackwardArgs a{};
+        if (int rc = classes_of("veda_bias_backward", spec, &a.b)) return rc;
+        if (workspace_bytes < veda_bias_backward_workspace_bytes(layout, n_heads, spec))
+            return fail(VEDA_ERR_INVALID, "veda_bias_backward: workspace smaller than veda_bias_backward_workspace_bytes()");
+        if (!aligned16(d_scores) || !aligned16(workspace) || !aligned16(d_bias))
+            return fail(VEDA_ERR_INVALID, "veda_bias_backward: buffers need 16-byte alignment");
+        if (int rc = check_size("veda_bias_backward", layout, n_heads)) return rc;
+        DeviceInfo di;
+        if (int rc = current_device(&di)) return rc;
+        const DeviceCopy* dc;
+        if (int rc = layout_on_device(layout, &dc)) return rc;
+        a.d_scores = d_scores;
+        a.tile_pos = reinterpret_cast<const int4*>(dc->tile_pos);
+        a.span_grid = reinterpret_cast<const int4*>(dc->span_grid);
+        a.partial = static_cast<float*>(workspace);
+        a.n = layout->desc.n_video;
+        a.rows_per_chunk = bias_chunk_rows(a.n);
+        const int chunks = bias_chunks(a.n);
+        const int smem = a.n * int(sizeof(float));
+        if (smem > 48 * 1024) {
+            cudaError_t e = cudaFuncSetAttribute(bias_backward_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+            if (e != cudaSuccess) return fail(VEDA_ERR_CUDA, std::string("cudaFuncSetAttribute(bias_backward_kernel): ") + cudaGetErrorString(e));
+        }
+        cudaStream_t s = static_cast<cudaStream_t>(stream);
+        bias_backward_kernel<<<dim3(chunks, n_heads), 256, smem, s>>>(a);
+        if (int rc = launch_status("bias_backward_kernel")) return rc;
+        bias_reduce_kernel<<<dim3((a.b.buckets + 255) / 256, n_heads), 256, 0, s>>>(a.partial, d_bias, chunks, a.b.buckets);
+        return launch_status("bias_reduce_kernel");
+    });
+}
+
+extern "C" int veda_distill(const veda_layout* layout, const float* scores, int32_t n_heads, const int32_t* t_idx,
+                            const float* t_val, const int32_t* t_cnt, int32_t width, int32_t by_column, float tau,
+                            const float* row_weight, float* loss, float* d_scores, void* stream) {
+    return guarded([&] {
+        clear_error();
+        if (!layout || !scores || !t_idx || !t_val || !t_cnt || !loss) return fail(VEDA_ERR_INVALID, "veda_distill: NULL argument");
+        if (n_heads <= 0 || width <= 0) return fail(VEDA_ERR_INVALID, "veda_distill: n_heads and width must be positive");
+        if (!(tau > 0.f) || !std::isfinite(tau) || !std::isfinite(1.f / tau))
+            return fail(VEDA_ERR_INVALID, "veda_distill: tau must be positive and finite, and so its inverse");
+        for (const void* p : {(const void*)scores, (const void*)t_idx, (const void*)t_val, (const void*)t_cnt,
+                              (const void*)row_weight, (const void*)loss, (const void*)d_scores})
+            if (!aligned16(p)) return fail(VEDA_ERR_INVALID, "veda_distill: buffers need 16-byte alignment");
+        if (int rc = check_size("veda_distill", layout, n_heads)) return rc;
+        DistillArgs a{};
+        a.n = layout->desc.n_video;
+        a.rows = int64_t(n_heads) * a.n;
+        const char *s0 = reinterpret_cast<const char*>(scores), *d0 = reinterpret_cast<const char*>(d_scores);
+        const int64_t bytes = a.rows * a.n * 4;
+        if (d_scores && d0 < s0 + bytes && s0 < d0 + bytes)
+            return fail(VEDA_ERR_INVALID, "veda_distill: d_scores must not overlap scores");
+        DeviceInfo di;
+        if (int rc = current_device(&di)) return rc;
+        a.scores = scores;
+        a.t_idx = t_idx;
+        a.t_val = t_val;
+        a.t_cnt = t_cnt;
+        a.row_weight = row_weight;
+        a.loss = loss;
+        a.d_scores = d_scores;
+        a.width = width;
+        a.n_tiles = layout->desc.n_tiles;
+        a.by_column = by_column;
+        a.inv_tau = 1.f / tau;
+        a.err = di.err;
+        distill_kernel<<<unsigned(a.rows), 128, 0, static_cast<cudaStream_t>(stream)>>>(a);
+        return launch_status("distill_kernel");
+    });
+}
+
+extern "C" size_t veda_score_backward_workspace_bytes(const veda_layout* layout, int32_t n_heads, int32_t dim) {
+    if (!layout || n_heads <= 0 || dim <= 0) return 0;
+    return round256(2 * size_t(n_heads) * size_t(layout->desc.n_video) * size_t(dim) * sizeof(float));
+}
+
+extern "C" int veda_score_backward(const veda_layout* layout, const float* feats_q, const float* feats_k, int32_t n_heads,
+                                   int32_t dim, const float* hats, const float* d_scores, float* d_proj_q,
+                                   float* d_proj_k, void* workspace, size_t workspace_bytes, void* stream) {
+    return guarded([&] {
+        clear_error();
+        if (!layout || !feats_q || !feats_k || !hats || !d_scores || !d_proj_q || !d_proj_k || !workspace)
+            return fail(VEDA_ERR_INVALID, "veda_score_backward: NULL argument");
+        if (int rc = check_heads("veda_score_backward", n_heads, dim)) return rc;
+        if (workspace_bytes < veda_score_backward_workspace_bytes(layout, n_heads, dim))
+            return fail(VEDA_ERR_INVALID, "veda_score_backward: workspace smaller than veda_score_backward_workspace_bytes()");
+        for (const void* p : {(const void*)feats_q, (const void*)feats_k, (const void*)hats, (const void*)d_scores,
+                              (const void*)d_proj_q, (const void*)d_proj_k, (const void*)workspace})
+            if (!aligned16(p)) return fail(VEDA_ERR_INVALID, "veda_score_backward: buffers need 16-byte alignment");
+        if (int rc = check_size("veda_score_backward", layout, n_heads)) return rc;
+        DeviceInfo di;
+        if (int rc = current_device(&di)) return rc;
+        const int n = layout->desc.n_video;
+        const int64_t nf = int64_t(n) * 3 * dim, nd = int64_t(n) * dim, nn = int64_t(n) * n;
+        float* dx = static_cast<float*>(workspace);
+        cudaStream_t s = static_cast<cudaStream_t>(stream);
+        const float c = float(1.0 / std::sqrt(double(dim)));
+        for (int side = 0; side < 2; ++side) {
+            // dq_hat = c dS k_hat; dk_hat = c dS^T q_hat
+            train::Operand<float> A{d_scores, nn, side ? 1 : n, side ? n : 1, n};
+            train::Operand<float> B{hats + (side ? 0 : n_heads * nd), nd, 1, dim, dim};
+            train::StoreEpilogue e{dx + side * n_heads * nd, nd, n, dim, c, nullptr, 0, 0};
+            train::gemm_kernel<<<dim3(1, (n + 127) / 128, n_heads), 256, 0, s>>>(A, B, n, e);
+            if (int rc = launch_status("score_backward gemm_kernel (projected features)")) return rc;
+            // dP = feats^T dx_hat
+            train::Operand<float> F{side ? feats_k : feats_q, nf, 1, 3 * dim, 3 * dim};
+            train::Operand<float> X{dx + side * n_heads * nd, nd, 1, dim, dim};
+            train::StoreEpilogue p{side ? d_proj_k : d_proj_q, 3 * int64_t(dim) * dim, 3 * dim, dim, 1.f, nullptr, 0, 0};
+            train::gemm_kernel<<<dim3(1, (3 * dim + 127) / 128, n_heads), 256, 0, s>>>(F, X, n, p);
+            if (int rc = launch_status("score_backward gemm_kernel (projections)")) return rc;
+        }
+        return VEDA_OK;
+    });
+}
