@@ -1,4 +1,4 @@
-// fp32 products of the predictor's scores with a bias, of their gradients and of the pooled teacher:
+// fp32 products of the predictor's scores with a bias and of their gradients:
 // C[batch] = epilogue(A[batch] B[batch]^T), 128 x 128 tiles, 256 threads with 8 x 8 sums each.
 #pragma once
 
@@ -85,38 +85,6 @@ struct BiasEpilogue {
                 }
                 C[(int64_t(batch) * n + m) * n + k] = c[i][j] * scale + b;
             }
-    }
-};
-
-// teacher[i][j] = max over the tile pair's real rows of scale * (AB^T) - lse[row]
-struct PoolEpilogue {
-    float* out;
-    int n;
-    float scale;
-    const int32_t* valid_count;
-    const int32_t* perm;
-    const float* lse;  // [n_heads, seq_len] or null
-    int64_t seq_len;
-    __device__ void operator()(float (&c)[8][8], int batch, int m0, int n0, int tm, int tn) const {
-        __shared__ float part[256];
-        const int ti = m0 >> 7, tj = n0 >> 7;
-        const int vi = valid_count[ti], vj = valid_count[tj];
-        float best = -INFINITY;
-        for (int i = 0; i < 8; ++i) {
-            if (tm + i >= vi) continue;
-            float off = 0.f;
-            if (lse) off = lse[batch * seq_len + perm[m0 + tm + i]];
-            if (!isfinite(off)) continue;
-            for (int j = 0; j < 8; ++j)
-                if (tn + j < vj) best = fmaxf(best, c[i][j] * scale - off);
-        }
-        part[threadIdx.x] = best;
-        __syncthreads();
-        for (int s = 128; s; s >>= 1) {
-            if (threadIdx.x < s) part[threadIdx.x] = fmaxf(part[threadIdx.x], part[threadIdx.x + s]);
-            __syncthreads();
-        }
-        if (threadIdx.x == 0) out[(int64_t(batch) * n + ti) * n + tj] = part[0];
     }
 };
 

@@ -164,6 +164,7 @@ int current_device(DeviceInfo* out) {
     return VEDA_OK;
 }
 int layout_on_device(const veda_layout* lay, const DeviceCopy** out) { return device_copy(lay, out); }
+int make_bf16_rows_map(CUtensorMap* m, const void* base, int64_t rows, int dim) { return make_tile_map(m, base, rows, dim); }
 uint64_t wait_timeout_ns() { return g_timeout_ns.load(); }
 int launch_status(const char* what) { return launch_check(what); }
 

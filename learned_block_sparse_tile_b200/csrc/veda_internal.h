@@ -1,6 +1,7 @@
 // Internal declarations of libveda (not part of the C ABI).
 #pragma once
 
+#include <cuda.h>
 #include <cuda_runtime.h>
 
 #include <cstdint>
@@ -52,6 +53,8 @@ int current_device(DeviceInfo* out);
 // Device copy of a layout's index data on the current device (made on first use).
 int layout_on_device(const veda_layout* lay, const DeviceCopy** out);
 uint64_t wait_timeout_ns();
+// TMA map over bf16 rows [rows, dim] in boxes of 128 rows x 64 columns with the 128-byte swizzle
+int make_bf16_rows_map(CUtensorMap* m, const void* base, int64_t rows, int dim);
 // `cudaGetLastError` after a launch, as a VEDA_* status
 int launch_status(const char* what);
 

@@ -4,6 +4,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 #include <cstring>
 #include <string>
@@ -11,6 +12,7 @@
 #include "veda_internal.h"
 #include "bias.cuh"
 #include "distill.cuh"
+#include "teacher.cuh"
 #include "train_gemm.cuh"
 
 using namespace veda;
@@ -75,6 +77,35 @@ int classes_of(const char* who, const veda_bias_spec* spec, BiasClasses* out) {
     return VEDA_OK;
 }
 
+// Key runs per group of query tiles. A unit costs its key pairs plus about one and a half pairs' time to load Q and
+// to fill and drain the pipeline; the runs are the number that makes the busiest CTA's sum least.
+int teacher_runs(int64_t groups, int pairs, int sms) {
+    int best = 1;
+    double least = 1e300;
+    for (int c = 1; c <= std::min(pairs, 64); ++c) {
+        const double cost = double((groups * c + sms - 1) / sms) * ((pairs + c - 1) / c + 1.5);
+        if (cost < least * 0.995) {
+            least = cost;
+            best = c;
+        }
+    }
+    return best;
+}
+
+template <int D>
+int launch_teacher(const teacher::Maps& m, const teacher::Args& a, const DeviceInfo& di, cudaStream_t s) {
+    static std::atomic<bool> set[kMaxDevices];
+    if (!set[di.ordinal].load()) {
+        cudaError_t e = cudaFuncSetAttribute(teacher::teacher_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             int(teacher::Cfg<D>::kSmem));
+        if (e != cudaSuccess)
+            return fail(VEDA_ERR_CUDA, std::string("cudaFuncSetAttribute(teacher_kernel): ") + cudaGetErrorString(e));
+        set[di.ordinal].store(true);
+    }
+    teacher::teacher_kernel<D><<<unsigned(std::min(a.units, di.sms)), teacher::kThreads, teacher::Cfg<D>::kSmem, s>>>(m, a);
+    return launch_status("teacher_kernel");
+}
+
 // query rows of one chunk of the bias gradient's sums: enough chunks to fill the GPU, few enough to add up
 int bias_chunk_rows(int n) { return std::max(1, (n + 31) / 32); }
 int bias_chunks(int n) { return (n + bias_chunk_rows(n) - 1) / bias_chunk_rows(n); }
@@ -126,12 +157,30 @@ extern "C" int veda_teacher(const veda_layout* layout, const void* q_t, const vo
         if (int rc = layout_on_device(layout, &dc)) return rc;
         const veda_layout_desc& d = layout->desc;
         const int n = d.n_video;
-        train::Operand<__nv_bfloat16> A{static_cast<const __nv_bfloat16*>(q_t), d.n_slots * dim, dim, 1, n * kTile};
-        train::Operand<__nv_bfloat16> B = A;
-        B.base = static_cast<const __nv_bfloat16*>(k_t);
-        train::PoolEpilogue e{teacher, n, float(1.0 / std::sqrt(double(dim))), dc->valid_count, dc->perm, row_lse, d.seq_len};
-        train::gemm_kernel<<<dim3(n, n, n_heads), 256, 0, static_cast<cudaStream_t>(stream)>>>(A, B, dim, e);
-        return launch_status("teacher gemm_kernel");
+        if (int64_t(n_heads) * d.n_slots > INT32_MAX)
+            return fail(VEDA_ERR_UNSUPPORTED, "veda_teacher: more than 2^31 tile-ordered rows");
+        teacher::Maps m;
+        if (int rc = make_bf16_rows_map(&m.q, q_t, n_heads * d.n_slots, dim)) return rc;
+        if (int rc = make_bf16_rows_map(&m.k, k_t, n_heads * d.n_slots, dim)) return rc;
+        teacher::Args a{};
+        a.valid_count = dc->valid_count;
+        a.perm = dc->perm;
+        a.lse = row_lse;
+        a.out = teacher;
+        a.seq_len = d.seq_len;
+        a.n = d.n_video;
+        a.n_tiles = d.n_tiles;
+        a.groups = (a.n + 1) / 2;
+        a.pairs = (a.n + 1) / 2;
+        a.runs = teacher_runs(int64_t(n_heads) * a.groups, a.pairs, di.sms);
+        if (int64_t(n_heads) * a.groups * a.runs > INT32_MAX)
+            return fail(VEDA_ERR_UNSUPPORTED, "veda_teacher: too many work units for one launch");
+        a.units = n_heads * a.groups * a.runs;
+        a.scale = float(1.0 / std::sqrt(double(dim)));
+        a.timeout_ns = wait_timeout_ns();
+        a.err = di.err;
+        cudaStream_t s = static_cast<cudaStream_t>(stream);
+        return dim == 128 ? launch_teacher<128>(m, a, di, s) : launch_teacher<64>(m, a, di, s);
     });
 }
 
