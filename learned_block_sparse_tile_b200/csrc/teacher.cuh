@@ -24,6 +24,7 @@
 #include <cstdint>
 
 #include "ptx.cuh"
+#include "wait.cuh"
 
 namespace veda {
 namespace teacher {
@@ -156,7 +157,7 @@ __global__ void __launch_bounds__(kThreads, 1) teacher_kernel(const __grid_const
         for (int u = blockIdx.x; u < a.units && !stop; u += gridDim.x, ++lu) {
             const Unit w(a, u);
             const int row0 = w.head * a.n_tiles * 128;
-            if (!__all_sync(0xffffffffu, ptx::mbar_wait(&B.q_empty, (lu & 1) ^ 1, abort_flag, tmo))) break;
+            if (!warp_wait(&B.q_empty, (lu & 1) ^ 1, abort_flag, tmo)) break;
             if (ptx::elect_one()) {
                 ptx::mbar_arrive_expect_tx(&B.q_full, C::kQBytes);
                 for (int t = 0; t < 2; ++t)  // the last group of an odd count takes its tile twice
@@ -167,7 +168,7 @@ __global__ void __launch_bounds__(kThreads, 1) teacher_kernel(const __grid_const
             __syncwarp();
             for (int p = w.p0; p < w.p1; ++p, ++g) {
                 const int s = g % kStages, ph = g / kStages;
-                if (!__all_sync(0xffffffffu, ptx::mbar_wait(&B.k_empty[s], (ph & 1) ^ 1, abort_flag, tmo))) {
+                if (!warp_wait(&B.k_empty[s], (ph & 1) ^ 1, abort_flag, tmo)) {
                     stop = true;
                     break;
                 }
@@ -198,17 +199,17 @@ __global__ void __launch_bounds__(kThreads, 1) teacher_kernel(const __grid_const
         bool stop = false;
         for (int u = blockIdx.x; u < a.units && !stop; u += gridDim.x, ++lu) {
             const Unit w(a, u);
-            if (!__all_sync(0xffffffffu, ptx::mbar_wait(&B.q_full, lu & 1, abort_flag, tmo))) break;
+            if (!warp_wait(&B.q_full, lu & 1, abort_flag, tmo)) break;
             for (int p = w.p0; p < w.p1; ++p, ++g) {
                 const int s = g % kStages, ph = g / kStages;
-                if (!__all_sync(0xffffffffu, ptx::mbar_wait(&B.k_full[s], ph & 1, abort_flag, tmo))) {
+                if (!warp_wait(&B.k_full[s], ph & 1, abort_flag, tmo)) {
                     stop = true;
                     break;
                 }
                 const uint32_t id = 2 * p + 1 < a.n ? kPair : kSingle;
                 const uint32_t kb = ptx::smem_addr(smem + C::kOffK + s * C::kStageBytes);
                 for (int t = 0; t < 2; ++t) {
-                    if (!__all_sync(0xffffffffu, ptx::mbar_wait(&B.acc_empty[t], (g & 1) ^ 1, abort_flag, tmo))) {
+                    if (!warp_wait(&B.acc_empty[t], (g & 1) ^ 1, abort_flag, tmo)) {
                         stop = true;
                         break;
                     }
@@ -241,7 +242,7 @@ __global__ void __launch_bounds__(kThreads, 1) teacher_kernel(const __grid_const
             float* out = a.out + (int64_t(w.head) * a.n + w.q0 + t) * a.n;
             for (int p = w.p0; p < w.p1; p += kBatch, ++batch) {
                 const int b = batch & 1;
-                if (!__all_sync(0xffffffffu, ptx::mbar_wait(&B.part_full[t][b], (batch >> 1) & 1, abort_flag, tmo))) {
+                if (!warp_wait(&B.part_full[t][b], (batch >> 1) & 1, abort_flag, tmo)) {
                     stop = true;
                     break;
                 }
@@ -267,12 +268,12 @@ __global__ void __launch_bounds__(kThreads, 1) teacher_kernel(const __grid_const
             for (int p = w.p0; p < w.p1; ++p, ++g) {
                 const int at = (p - w.p0) % kBatch, b = batch & 1;
                 if (at == 0 &&
-                    !__all_sync(0xffffffffu, ptx::mbar_wait(&B.part_empty[t][b], ((batch >> 1) & 1) ^ 1, abort_flag, tmo))) {
+                    !warp_wait(&B.part_empty[t][b], ((batch >> 1) & 1) ^ 1, abort_flag, tmo)) {
                     stop = true;
                     break;
                 }
                 const int j0 = 2 * p, vj0 = a.valid_count[j0], vj1 = j0 + 1 < a.n ? a.valid_count[j0 + 1] : 0;
-                if (!__all_sync(0xffffffffu, ptx::mbar_wait(&B.acc_full[t], g & 1, abort_flag, tmo))) {
+                if (!warp_wait(&B.acc_full[t], g & 1, abort_flag, tmo)) {
                     stop = true;
                     break;
                 }

@@ -106,6 +106,30 @@ int launch_teacher(const teacher::Maps& m, const teacher::Args& a, const DeviceI
     return launch_status("teacher_kernel");
 }
 
+train::Operand operand(const float* base, int64_t batch, int64_t stride, int rows, bool cols) {
+    const bool whole = stride % 4 == 0 && batch % 4 == 0;
+    return {base, batch, stride, rows, cols ? train::kCols : whole ? train::kRowsVec : train::kRows};
+}
+
+int launch_gemm(const char* what, train::Args a, const DeviceInfo& di, cudaStream_t s) {
+    static std::atomic<bool> set[kMaxDevices];
+    if (!set[di.ordinal].load()) {
+        cudaError_t e = cudaFuncSetAttribute(train::gemm_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(train::kSmem));
+        if (e != cudaSuccess)
+            return fail(VEDA_ERR_CUDA, std::string("cudaFuncSetAttribute(train gemm_kernel): ") + cudaGetErrorString(e));
+        set[di.ordinal].store(true);
+    }
+    a.tiles_m = (a.M + train::kBM - 1) / train::kBM;
+    a.tiles_n = (a.N + train::kBN - 1) / train::kBN;
+    const int64_t tiles = int64_t(a.n_sets) * a.nb * a.tiles_m * a.tiles_n;
+    if (tiles > INT32_MAX) return fail(VEDA_ERR_UNSUPPORTED, std::string(what) + ": too many tiles for one launch");
+    a.n_tiles = int(tiles);
+    a.timeout_ns = wait_timeout_ns();
+    a.err = di.err;
+    train::gemm_kernel<<<unsigned(std::min(a.n_tiles, di.sms)), train::kThreads, train::kSmem, s>>>(a);
+    return launch_status(what);
+}
+
 // query rows of one chunk of the bias gradient's sums: enough chunks to fill the GPU, few enough to add up
 int bias_chunk_rows(int n) { return std::max(1, (n + 31) / 32); }
 int bias_chunks(int n) { return (n + bias_chunk_rows(n) - 1) / bias_chunk_rows(n); }
@@ -221,19 +245,32 @@ extern "C" int veda_score_bias(const veda_layout* layout, const float* feats_q, 
             if (int rc = launch_status("bias_expand_kernel")) return rc;
         }
         const int64_t nf = int64_t(n) * 3 * dim, nd = int64_t(n) * dim;
+        train::Args p{};
+        p.n_sets = 2;
+        p.nb = n_heads;
+        p.M = n;
+        p.N = dim;
+        p.K = 3 * dim;
+        p.scale = 1.f;
         for (int side = 0; side < 2; ++side) {
             const float* f = side ? feats_k : feats_q;
-            train::Operand<float> A{f, nf, 3 * dim, 1, n};
-            train::Operand<float> B{side ? proj_k : proj_q, 3 * int64_t(dim) * dim, 1, dim, dim};
-            train::StoreEpilogue e{hats + side * n_heads * nd, nd, n, dim, 1.f, f, nf, 3 * dim};
-            train::gemm_kernel<<<dim3(1, (n + 127) / 128, n_heads), 256, 0, s>>>(A, B, 3 * dim, e);
-            if (int rc = launch_status("score_bias gemm_kernel (projections)")) return rc;
+            p.set[side] = {operand(f, nf, 3 * dim, n, false),
+                           operand(side ? proj_k : proj_q, 3 * int64_t(dim) * dim, dim, dim, true),
+                           hats + side * n_heads * nd, f, nf, 3 * dim};
         }
-        train::Operand<float> A{hats, nd, dim, 1, n}, B{hats + n_heads * nd, nd, dim, 1, n};
-        train::BiasEpilogue e{scores, n, float(1.0 / std::sqrt(double(dim))), bias ? table : nullptr, offsets + 2,
-                              reinterpret_cast<const int4*>(dc->tile_num), offsets};
-        train::gemm_kernel<<<dim3((n + 127) / 128, (n + 127) / 128, n_heads), 256, 0, s>>>(A, B, dim, e);
-        return launch_status("score_bias gemm_kernel (logits)");
+        if (int rc = launch_gemm("veda_score_bias (projections)", p, di, s)) return rc;
+        train::Args l{};
+        l.n_sets = 1;
+        l.nb = n_heads;
+        l.M = l.N = n;
+        l.K = dim;
+        l.scale = float(1.0 / std::sqrt(double(dim)));
+        l.set[0] = {operand(hats, nd, dim, n, false), operand(hats + n_heads * nd, nd, dim, n, false), scores, nullptr, 0, 0};
+        if (bias) l.table = table;
+        l.tile_num = reinterpret_cast<const int4*>(dc->tile_num);
+        l.table_stride = offsets + 2;
+        l.offsets = offsets;
+        return launch_gemm("veda_score_bias (logits)", l, di, s);
     });
 }
 
@@ -346,20 +383,22 @@ extern "C" int veda_score_backward(const veda_layout* layout, const float* feats
         float* dx = static_cast<float*>(workspace);
         cudaStream_t s = static_cast<cudaStream_t>(stream);
         const float c = float(1.0 / std::sqrt(double(dim)));
+        // dq_hat = c dS k_hat and dk_hat = c dS^T q_hat, then dP = feats^T dx_hat, both sides in one launch
+        train::Args x{}, p{};
+        x.n_sets = p.n_sets = 2;
+        x.nb = p.nb = n_heads;
+        x.M = x.K = p.K = n;
+        x.N = p.N = dim;
+        p.M = 3 * dim;
+        x.scale = c;
+        p.scale = 1.f;
         for (int side = 0; side < 2; ++side) {
-            // dq_hat = c dS k_hat; dk_hat = c dS^T q_hat
-            train::Operand<float> A{d_scores, nn, side ? 1 : n, side ? n : 1, n};
-            train::Operand<float> B{hats + (side ? 0 : n_heads * nd), nd, 1, dim, dim};
-            train::StoreEpilogue e{dx + side * n_heads * nd, nd, n, dim, c, nullptr, 0, 0};
-            train::gemm_kernel<<<dim3(1, (n + 127) / 128, n_heads), 256, 0, s>>>(A, B, n, e);
-            if (int rc = launch_status("score_backward gemm_kernel (projected features)")) return rc;
-            // dP = feats^T dx_hat
-            train::Operand<float> F{side ? feats_k : feats_q, nf, 1, 3 * dim, 3 * dim};
-            train::Operand<float> X{dx + side * n_heads * nd, nd, 1, dim, dim};
-            train::StoreEpilogue p{side ? d_proj_k : d_proj_q, 3 * int64_t(dim) * dim, 3 * dim, dim, 1.f, nullptr, 0, 0};
-            train::gemm_kernel<<<dim3(1, (3 * dim + 127) / 128, n_heads), 256, 0, s>>>(F, X, n, p);
-            if (int rc = launch_status("score_backward gemm_kernel (projections)")) return rc;
+            x.set[side] = {operand(d_scores, nn, n, n, side == 1), operand(hats + (side ? 0 : n_heads * nd), nd, dim, dim, true),
+                           dx + side * n_heads * nd, nullptr, 0, 0};
+            p.set[side] = {operand(side ? feats_k : feats_q, nf, 3 * dim, 3 * dim, true),
+                           operand(dx + side * n_heads * nd, nd, dim, dim, true), side ? d_proj_k : d_proj_q, nullptr, 0, 0};
         }
-        return VEDA_OK;
+        if (int rc = launch_gemm("veda_score_backward (projected features)", x, di, s)) return rc;
+        return launch_gemm("veda_score_backward (projections)", p, di, s);
     });
 }
