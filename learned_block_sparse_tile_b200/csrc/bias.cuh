@@ -70,9 +70,10 @@ __global__ void __launch_bounds__(256) bias_expand_kernel(const float* bias, flo
 struct BiasBackwardArgs {
     const float* d_scores;     // [n_heads, n, n]
     const int4* tile_pos;      // [n] {span, t, h, w}
+    const int4* tile_num;      // [n] {span, number as key, number as query, 0}
     const int4* span_grid;     // [n_spans] {first tile, tiles along t, h, w}
     float* partial;            // [n_heads, chunks, buckets]
-    int n, rows_per_chunk;
+    int n, n_spans, offsets, rows_per_chunk;
     BiasClasses b;
 };
 
@@ -99,9 +100,99 @@ __device__ __forceinline__ void bias_interval(const int* starts, int reach, int 
     hi = min(hi, count);
 }
 
-// Sums of one chunk of query rows: each bucket of a row is a box of its span's tile array (the classes are
-// intervals of the offset), and a thread adds its buckets' boxes in a fixed order, so nothing is atomic.
-__global__ void __launch_bounds__(256) bias_backward_kernel(const BiasBackwardArgs a) {
+// Sums of one chunk of query rows, by offset first. Within a row no two keys of the query's span have the same offset, so
+// a row adds to as many different sums as it has columns: the CTA keeps one sum per offset in shared memory (fewer than 8
+// per tile), its threads add a row's columns without collisions, and a barrier parts the rows. Nothing is atomic, and
+// every sum is added up in row order. The loads run kDepth rows ahead in registers, because the rows' own work is short:
+// an addition in shared memory and a barrier. At the end each bucket is the sum of a box of offsets.
+// Bound by the barriers, about 100 cycles a row, with two CTAs on an SM taking turns; reading d_scores is the floor.
+template <int kPer>
+__global__ void __launch_bounds__(512, kPer <= 4 ? 2 : 1) bias_backward_kernel(const BiasBackwardArgs a) {
+    constexpr int kDepth = kPer <= 2 ? 8 : kPer <= 4 ? 4 : 2;
+    extern __shared__ float sums[];  // [offsets], then 2 x 16 for the cross-span sums of the warps
+    const int head = blockIdx.y, pairs = a.b.buckets - 2, nt = blockDim.x;
+    const int i0 = blockIdx.x * a.rows_per_chunk, i1 = min(a.n, i0 + a.rows_per_chunk);
+    const float* src = a.d_scores + int64_t(head) * a.n * a.n;
+    float v[kDepth][kPer];
+    int span[kPer], num[kPer];
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) {
+        const int j = threadIdx.x + nt * k;
+        const int4 key = a.tile_num[min(j, a.n - 1)];
+        span[k] = j < a.n ? key.x : -1;
+        num[k] = key.y;
+    }
+    const auto load = [&](float (&x)[kPer], int i) {
+#pragma unroll
+        for (int k = 0; k < kPer; ++k) {
+            const int j = threadIdx.x + nt * k;
+            x[k] = j < a.n && i < i1 ? __ldg(src + int64_t(i) * a.n + j) : 0.f;
+        }
+    };
+#pragma unroll
+    for (int r = 0; r < kDepth; ++r) load(v[r], i0 + r);
+    for (int o = threadIdx.x; o < a.offsets; o += nt) sums[o] = 0.f;
+    __syncthreads();
+    float before = 0.f, behind = 0.f;
+    for (int i = i0; i < i1; i += kDepth) {
+#pragma unroll
+        for (int r = 0; r < kDepth; ++r) {
+            if (i + r < i1) {
+                const int4 query = a.tile_num[i + r];
+#pragma unroll
+                for (int k = 0; k < kPer; ++k) {
+                    if (span[k] == query.x) {
+                        sums[num[k] + query.z] += v[r][k];
+                    } else {  // (threads past the row hold zeros)
+                        before += span[k] < query.x ? v[r][k] : 0.f;
+                        behind += span[k] > query.x ? v[r][k] : 0.f;
+                    }
+                }
+                load(v[r], i + r + kDepth);
+                __syncthreads();
+            }
+        }
+    }
+    float* cross = sums + a.offsets;
+#pragma unroll
+    for (int o = 16; o; o >>= 1) {
+        before += __shfl_xor_sync(0xffffffffu, before, o);
+        behind += __shfl_xor_sync(0xffffffffu, behind, o);
+    }
+    if ((threadIdx.x & 31) == 0) {
+        cross[threadIdx.x >> 5] = before;
+        cross[16 + (threadIdx.x >> 5)] = behind;
+    }
+    __syncthreads();
+    float* out = a.partial + (int64_t(head) * gridDim.x + blockIdx.x) * a.b.buckets;
+    const int ih = 2 * a.b.reach[1] - 1, iw = 2 * a.b.reach[2] - 1;
+    for (int b = threadIdx.x; b < a.b.buckets; b += nt) {
+        float sum = 0.f;
+        if (b >= pairs) {
+            for (int w = 0; w < nt / 32; ++w) sum += cross[16 * (b - pairs) + w];
+        } else {
+            const float* at = sums;
+            for (int s = 0; s < a.n_spans; ++s) {
+                const int4 g = a.span_grid[s];
+                const int rt = 2 * g.y - 1, rh = 2 * g.z - 1, rw = 2 * g.w - 1;
+                int t0, t1, h0, h1, w0, w1;
+                bias_interval(a.b.starts[0], a.b.reach[0], b / (iw * ih), g.y - 1, rt, t0, t1);
+                bias_interval(a.b.starts[1], a.b.reach[1], (b / iw) % ih, g.z - 1, rh, h0, h1);
+                bias_interval(a.b.starts[2], a.b.reach[2], b % iw, g.w - 1, rw, w0, w1);
+                for (int t = t0; t < t1; ++t)
+                    for (int h = h0; h < h1; ++h)
+                        for (int w = w0; w < w1; ++w) sum += at[(t * rh + h) * rw + w];
+                at += rt * rh * rw;
+            }
+        }
+        out[b] = sum;
+    }
+}
+
+// The same for layouts of so many tiles that their offsets do not fit a CTA's shared memory (over 7000 tiles): each
+// bucket of a row is a box of its span's tile array (the classes are intervals of the offset), and a thread adds
+// its buckets' boxes in a fixed order.
+__global__ void __launch_bounds__(256) bias_backward_wide_kernel(const BiasBackwardArgs a) {
     extern __shared__ float row[];
     const int head = blockIdx.y, pairs = a.b.buckets - 2;
     const int i0 = blockIdx.x * a.rows_per_chunk, i1 = min(a.n, i0 + a.rows_per_chunk);

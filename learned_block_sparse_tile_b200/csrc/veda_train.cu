@@ -130,9 +130,32 @@ int launch_gemm(const char* what, train::Args a, const DeviceInfo& di, cudaStrea
     return launch_status(what);
 }
 
-// query rows of one chunk of the bias gradient's sums: enough chunks to fill the GPU, few enough to add up
-int bias_chunk_rows(int n) { return std::max(1, (n + 31) / 32); }
-int bias_chunks(int n) { return (n + bias_chunk_rows(n) - 1) / bias_chunk_rows(n); }
+// Query rows of one chunk of the bias gradient's sums: with all heads about two CTAs for each of 148 SMs, but not fewer
+// than eight rows, which a chunk's own start and end cost.
+int bias_chunk_rows(int n, int n_heads) {
+    const int chunks = std::max(1, std::min(296 / std::max(n_heads, 1), (n + 7) / 8));
+    return std::max(1, (n + chunks - 1) / chunks);
+}
+int bias_chunks(int n, int n_heads) {
+    const int rows = bias_chunk_rows(n, n_heads);
+    return (n + rows - 1) / rows;
+}
+
+constexpr int kBiasMaxSmem = 227 * 1024;
+
+template <int kPer>
+int launch_bias_backward(const BiasBackwardArgs& a, int chunks, int n_heads, const DeviceInfo& di, cudaStream_t s) {
+    static std::atomic<bool> set[kMaxDevices];
+    if (!set[di.ordinal].load()) {
+        cudaError_t e = cudaFuncSetAttribute(bias_backward_kernel<kPer>, cudaFuncAttributeMaxDynamicSharedMemorySize, kBiasMaxSmem);
+        if (e != cudaSuccess)
+            return fail(VEDA_ERR_CUDA, std::string("cudaFuncSetAttribute(bias_backward_kernel): ") + cudaGetErrorString(e));
+        set[di.ordinal].store(true);
+    }
+    const int threads = std::min(512, std::max(128, (a.n + 31) / 32 * 32));
+    bias_backward_kernel<kPer><<<dim3(chunks, n_heads), threads, (a.offsets + 32) * sizeof(float), s>>>(a);
+    return launch_status("bias_backward_kernel");
+}
 
 }  // namespace
 
@@ -180,7 +203,6 @@ extern "C" int veda_teacher(const veda_layout* layout, const void* q_t, const vo
         const DeviceCopy* dc;
         if (int rc = layout_on_device(layout, &dc)) return rc;
         const veda_layout_desc& d = layout->desc;
-        const int n = d.n_video;
         if (int64_t(n_heads) * d.n_slots > INT32_MAX)
             return fail(VEDA_ERR_UNSUPPORTED, "veda_teacher: more than 2^31 tile-ordered rows");
         teacher::Maps m;
@@ -277,7 +299,7 @@ extern "C" int veda_score_bias(const veda_layout* layout, const float* feats_q, 
 extern "C" size_t veda_bias_backward_workspace_bytes(const veda_layout* layout, int32_t n_heads, const veda_bias_spec* spec) {
     BiasClasses b;
     if (!layout || n_heads <= 0 || guarded([&] { return classes_of("veda_bias_backward_workspace_bytes", spec, &b); })) return 0;
-    return round256(size_t(n_heads) * bias_chunks(layout->desc.n_video) * size_t(b.buckets) * sizeof(float));
+    return round256(size_t(n_heads) * bias_chunks(layout->desc.n_video, n_heads) * size_t(b.buckets) * sizeof(float));
 }
 
 extern "C" int veda_bias_backward(const veda_layout* layout, const float* d_scores, int32_t n_heads,
@@ -303,16 +325,28 @@ extern "C" int veda_bias_backward(const veda_layout* layout, const float* d_scor
         a.span_grid = reinterpret_cast<const int4*>(dc->span_grid);
         a.partial = static_cast<float*>(workspace);
         a.n = layout->desc.n_video;
-        a.rows_per_chunk = bias_chunk_rows(a.n);
-        const int chunks = bias_chunks(a.n);
-        const int smem = a.n * int(sizeof(float));
-        if (smem > 48 * 1024) {
-            cudaError_t e = cudaFuncSetAttribute(bias_backward_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-            if (e != cudaSuccess) return fail(VEDA_ERR_CUDA, std::string("cudaFuncSetAttribute(bias_backward_kernel): ") + cudaGetErrorString(e));
-        }
+        a.tile_num = reinterpret_cast<const int4*>(dc->tile_num);
+        a.n_spans = int(layout->span_grid.size() / 4);
+        a.offsets = layout->bias_offsets;
+        a.rows_per_chunk = bias_chunk_rows(a.n, n_heads);
+        const int chunks = bias_chunks(a.n, n_heads);
         cudaStream_t s = static_cast<cudaStream_t>(stream);
-        bias_backward_kernel<<<dim3(chunks, n_heads), 256, smem, s>>>(a);
-        if (int rc = launch_status("bias_backward_kernel")) return rc;
+        int rc;
+        if ((a.offsets + 32) * int(sizeof(float)) > kBiasMaxSmem || a.n > 8192) {
+            const int smem = a.n * int(sizeof(float));
+            cudaError_t e = cudaFuncSetAttribute(bias_backward_wide_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+            if (e != cudaSuccess)
+                return fail(VEDA_ERR_CUDA, std::string("cudaFuncSetAttribute(bias_backward_wide_kernel): ") + cudaGetErrorString(e));
+            bias_backward_wide_kernel<<<dim3(chunks, n_heads), 256, smem, s>>>(a);
+            rc = launch_status("bias_backward_wide_kernel");
+        } else {
+            rc = a.n <= 512    ? launch_bias_backward<1>(a, chunks, n_heads, di, s)
+                 : a.n <= 1024 ? launch_bias_backward<2>(a, chunks, n_heads, di, s)
+                 : a.n <= 2048 ? launch_bias_backward<4>(a, chunks, n_heads, di, s)
+                 : a.n <= 4096 ? launch_bias_backward<8>(a, chunks, n_heads, di, s)
+                               : launch_bias_backward<16>(a, chunks, n_heads, di, s);
+        }
+        if (rc) return rc;
         bias_reduce_kernel<<<dim3((a.b.buckets + 255) / 256, n_heads), 256, 0, s>>>(a.partial, d_bias, chunks, a.b.buckets);
         return launch_status("bias_reduce_kernel");
     });

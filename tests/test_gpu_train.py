@@ -183,6 +183,24 @@ def test_bias_backward(geo, heads, reach, far):
     within(bias_backward(geo, ds, reach, far), sums(ds.double()), (3 * geo.n + 64) * EPS * sums(ds.double().abs()))
 
 
+@pytest.mark.parametrize("spans,heads", [([((13, 48, 84), (1, 8, 16))], 2), ([((61, 45, 80), (8, 1, 16))], 1),
+                                         ([((4000, 1, 1), (1, 1, 128))], 1), ([((29, 90, 160), (1, 8, 16)), ((7, 64, 64), (2, 8, 8))], 1),
+                                         ([((7300, 1, 1), (1, 1, 128))], 1), ([((72, 80, 170), (1, 8, 16))], 1)])
+def test_bias_backward_wide_layouts(spans, heads):
+    # every width of the kernel: 468, 1800, 4000, 3686 + 224, 7300 tiles, and 7920 tiles whose offsets fit no shared memory
+    geo, reach, far = Geometry(spans), (4, 4, 6), (16, 16, 32)
+    ds = randn(1, heads, geo.n, geo.n)
+    total = L.veda_bias_buckets(reach, far)
+    index = torch.as_tensor(L.veda_bias_index(geo.layout, reach, far), device=DEV).long().reshape(-1)
+
+    def sums(x):
+        return torch.zeros(heads, total, dtype=torch.float64, device=DEV).index_add_(1, index, x.reshape(heads, -1))
+
+    got = bias_backward(geo, ds, reach, far)
+    within(got, sums(ds.double()), (3 * geo.n + 64) * EPS * sums(ds.double().abs()))
+    assert torch.equal(bias_backward(geo, ds, reach, far), got)
+
+
 # --------------------------------------------------------------------------------------------- distillation
 
 
