@@ -106,7 +106,7 @@ __device__ __forceinline__ void bias_interval(const int* starts, int reach, int 
 // every sum is added up in row order. The loads run kDepth rows ahead in registers, because the rows' own work is short:
 // an addition in shared memory and a barrier. At the end each bucket is the sum of a box of offsets.
 // Bound by the barriers, about 100 cycles a row, with two CTAs on an SM taking turns; reading d_scores is the floor.
-template <int kPer>
+template <int kPer, bool kOneSpan>
 __global__ void __launch_bounds__(512, kPer <= 4 ? 2 : 1) bias_backward_kernel(const BiasBackwardArgs a) {
     constexpr int kDepth = kPer <= 2 ? 8 : kPer <= 4 ? 4 : 2;
     extern __shared__ float sums[];  // [offsets], then 2 x 16 for the cross-span sums of the warps
@@ -114,6 +114,7 @@ __global__ void __launch_bounds__(512, kPer <= 4 ? 2 : 1) bias_backward_kernel(c
     const int i0 = blockIdx.x * a.rows_per_chunk, i1 = min(a.n, i0 + a.rows_per_chunk);
     const float* src = a.d_scores + int64_t(head) * a.n * a.n;
     float v[kDepth][kPer];
+    int2 query[kDepth];  // {span, number} of the rows in flight
     int span[kPer], num[kPer];
 #pragma unroll
     for (int k = 0; k < kPer; ++k) {
@@ -122,15 +123,16 @@ __global__ void __launch_bounds__(512, kPer <= 4 ? 2 : 1) bias_backward_kernel(c
         span[k] = j < a.n ? key.x : -1;
         num[k] = key.y;
     }
-    const auto load = [&](float (&x)[kPer], int i) {
+    const auto load = [&](float (&x)[kPer], int2& q, int i) {
+        if (i >= i1) return;
+        const int4 t = a.tile_num[i];
+        q = make_int2(t.x, t.z);
+        const float* p = src + int64_t(i) * a.n + threadIdx.x;
 #pragma unroll
-        for (int k = 0; k < kPer; ++k) {
-            const int j = threadIdx.x + nt * k;
-            x[k] = j < a.n && i < i1 ? __ldg(src + int64_t(i) * a.n + j) : 0.f;
-        }
+        for (int k = 0; k < kPer; ++k) x[k] = threadIdx.x + nt * k < a.n ? __ldg(p + nt * k) : 0.f;
     };
 #pragma unroll
-    for (int r = 0; r < kDepth; ++r) load(v[r], i0 + r);
+    for (int r = 0; r < kDepth; ++r) load(v[r], query[r], i0 + r);
     for (int o = threadIdx.x; o < a.offsets; o += nt) sums[o] = 0.f;
     __syncthreads();
     float before = 0.f, behind = 0.f;
@@ -138,17 +140,16 @@ __global__ void __launch_bounds__(512, kPer <= 4 ? 2 : 1) bias_backward_kernel(c
 #pragma unroll
         for (int r = 0; r < kDepth; ++r) {
             if (i + r < i1) {
-                const int4 query = a.tile_num[i + r];
 #pragma unroll
                 for (int k = 0; k < kPer; ++k) {
-                    if (span[k] == query.x) {
-                        sums[num[k] + query.z] += v[r][k];
-                    } else {  // (threads past the row hold zeros)
-                        before += span[k] < query.x ? v[r][k] : 0.f;
-                        behind += span[k] > query.x ? v[r][k] : 0.f;
+                    if (kOneSpan ? span[k] >= 0 : span[k] == query[r].x) {
+                        sums[num[k] + query[r].y] += v[r][k];
+                    } else if (!kOneSpan) {  // (threads past the row hold zeros)
+                        before += span[k] < query[r].x ? v[r][k] : 0.f;
+                        behind += span[k] > query[r].x ? v[r][k] : 0.f;
                     }
                 }
-                load(v[r], i + r + kDepth);
+                load(v[r], query[r], i + r + kDepth);
                 __syncthreads();
             }
         }

@@ -6,12 +6,20 @@
 // With ms, mt the maxima of s / tau and t / tau, Zs and Zt the sums of exp(. - max):
 //     L = sum_list p ((t / tau - mt) - (s / tau - ms)) - log Zt + log Zs,
 // differences of numbers near zero, where log p - log q would cancel two long logarithms.
+//
+// The floor is one read of the scores and one write of their gradient (8 n bytes a row), so a row stays in registers
+// between them: up to 32 columns a thread, one warp for a row of up to 1024 columns and 2 to 16 warps beyond. Its
+// exponentials are taken once (2^x of (s - max) log2(e) / tau), serve both the sum and the gradient, and only the
+// listed columns, a tenth of the row or less, are visited again: they are written as q, and after a barrier as q - p.
+// Lists are read three times (largest logit, sums, gradient) and come from L1 after the first.
 #pragma once
 
 #include <cuda_runtime.h>
 
 #include <cmath>
 #include <cstdint>
+
+#include "ptx.cuh"
 
 namespace veda {
 
@@ -31,78 +39,119 @@ struct DistillArgs {
     int* err;
 };
 
-template <class Op>
-__device__ __forceinline__ float block_reduce_128(float v, float* scratch, Op op) {
+// One value for the row's kWarps warps. `scratch` holds kWarps floats, free again for the next reduction but one.
+template <int kWarps, class Op>
+__device__ __forceinline__ float row_reduce(float v, float* scratch, Op op) {
 #pragma unroll
     for (int o = 16; o; o >>= 1) v = op(v, __shfl_xor_sync(0xffffffffu, v, o));
-    __syncthreads();
-    if ((threadIdx.x & 31) == 0) scratch[threadIdx.x >> 5] = v;
-    __syncthreads();
-    return op(op(scratch[0], scratch[1]), op(scratch[2], scratch[3]));
+    if constexpr (kWarps > 1) {
+        if ((threadIdx.x & 31) == 0) scratch[threadIdx.x >> 5] = v;
+        __syncthreads();
+        v = scratch[0];
+#pragma unroll
+        for (int w = 1; w < kWarps; ++w) v = op(v, scratch[w]);
+    }
+    return v;
 }
 
-// One CTA per row.
-__global__ void __launch_bounds__(128) distill_kernel(const DistillArgs a) {
-    __shared__ float scratch[4];
+// Rows of up to 32 * kPer * kWarps columns. One warp per row: four rows in a CTA; else one row in a CTA.
+template <int kPer, int kWarps>
+__global__ void __launch_bounds__(kWarps == 1 ? 128 : 32 * kWarps) distill_kernel(const DistillArgs a) {
+    constexpr int kLanes = 32 * kWarps;
+    __shared__ float scratch[2][kWarps];
     __shared__ int s_cnt;
-    const int64_t r = blockIdx.x;
+    const int64_t r = kWarps == 1 ? int64_t(blockIdx.x) * 4 + (threadIdx.x >> 5) : int64_t(blockIdx.x);
+    if (kWarps == 1 && r >= a.rows) return;
+    const int lane = kWarps == 1 ? threadIdx.x & 31 : threadIdx.x;
     const float* s = a.scores + r * a.n;
     const int32_t* idx = a.t_idx + r * a.width;
     const float* val = a.t_val + r * (a.by_column ? a.n : a.width);
     const auto maxf = [](float x, float y) { return fmaxf(x, y); };
     const auto add = [](float x, float y) { return x + y; };
-    // the list: its entries are ascending tile ids; it is cut at the first bad one, and ids from n on
-    // (global tiles, which no score column stands for) end the part that counts
-    if (threadIdx.x == 0) s_cnt = max(0, min(a.t_cnt[r], a.width));
-    __syncthreads();
-    const int given = s_cnt;
-    bool bad = a.t_cnt[r] < 0 || a.t_cnt[r] > a.width;
-    __syncthreads();
-    for (int e = threadIdx.x; e < given; e += 128) {
-        const int id = idx[e];
-        const bool wrong = id < 0 || id >= a.n_tiles || (e > 0 && id <= idx[e - 1]);
-        if (wrong) bad = true;
-        if (wrong || id >= a.n) atomicMin(&s_cnt, e);
-    }
-    if (bad) atomicOr(a.err, kErrDistillList);
-    __syncthreads();
-    const int cnt = s_cnt;
 
-    float ms = -INFINITY;
-    for (int j = threadIdx.x; j < a.n; j += 128) ms = fmaxf(ms, s[j] * a.inv_tau);
-    ms = block_reduce_128(ms, scratch, maxf);
+    float v[kPer];
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) {
+        const int j = lane + kLanes * k;
+        v[k] = j < a.n ? __ldg(s + j) : -INFINITY;
+    }
+    // the list: its entries are ascending tile ids; it is cut at the first bad one, and ids from n on (global tiles,
+    // which no score column stands for) end the part that counts
+    const int given = a.t_cnt[r];
+    bool bad = given < 0 || given > a.width;
+    int cnt = max(0, min(given, a.width));
     float mt = -INFINITY;
-    for (int e = threadIdx.x; e < cnt; e += 128) mt = fmaxf(mt, val[a.by_column ? idx[e] : e] * a.inv_tau);
-    mt = block_reduce_128(mt, scratch, maxf);
-    float zs = 0.f, zt = 0.f, gap = 0.f;
-    for (int j = threadIdx.x; j < a.n; j += 128) {
-        const float x = s[j] * a.inv_tau;
-        zs += x == -INFINITY ? 0.f : expf(x - ms);
+    {
+        int end = cnt;
+        for (int e = lane; e < cnt; e += kLanes) {
+            const int id = idx[e];
+            const bool wrong = id < 0 || id >= a.n_tiles || (e > 0 && id <= idx[e - 1]);
+            bad |= wrong;
+            if (wrong || id >= a.n) {
+                end = e;
+                break;
+            }
+        }
+        if constexpr (kWarps == 1) {
+            cnt = __reduce_min_sync(0xffffffffu, end);
+        } else {
+            if (threadIdx.x == 0) s_cnt = cnt;
+            __syncthreads();
+            if (end < cnt) atomicMin(&s_cnt, end);
+            __syncthreads();
+            cnt = s_cnt;
+        }
+        if (bad) atomicOr(a.err, kErrDistillList);
     }
-    zs = block_reduce_128(zs, scratch, add);
-    for (int e = threadIdx.x; e < cnt; e += 128) {
-        const float t = val[a.by_column ? idx[e] : e] * a.inv_tau;
+    for (int e = lane; e < cnt; e += kLanes) mt = fmaxf(mt, val[a.by_column ? idx[e] : e]);
+    float ms = -INFINITY;
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) ms = fmaxf(ms, v[k]);
+    ms = row_reduce<kWarps>(ms, scratch[0], maxf);
+    mt = row_reduce<kWarps>(mt, scratch[1], maxf);
+
+    const float c2 = a.inv_tau * 1.4426950408889634f;
+    float zs = 0.f;
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) {
+        // (a column of -inf, or one past the row, has no mass, whatever the maximum is)
+        v[k] = v[k] == -INFINITY ? 0.f : ptx::ex2((v[k] - ms) * c2);
+        zs += v[k];
+    }
+    float zt = 0.f, gap = 0.f;
+    for (int e = lane; e < cnt; e += kLanes) {
+        const int id = idx[e];
+        const float t = val[a.by_column ? id : e];
         if (t == -INFINITY) continue;
-        const float p = expf(t - mt);
+        const float p = ptx::ex2((t - mt) * c2);
         zt += p;
-        if (p > 0.f) gap += p * ((t - mt) - (s[idx[e]] * a.inv_tau - ms));
+        if (!(p == 0.f)) gap += p * (((t - mt) - (__ldg(s + id) - ms)) * a.inv_tau);
     }
-    zt = block_reduce_128(zt, scratch, add);
-    gap = block_reduce_128(gap, scratch, add);
+    zs = row_reduce<kWarps>(zs, scratch[0], add);
+    zt = row_reduce<kWarps>(zt, scratch[1], add);
+    if constexpr (kWarps > 1) __syncthreads();
+    gap = row_reduce<kWarps>(gap, scratch[0], add);
     // no target (an empty list, or only -inf in it) or no student column above -inf: the row is left out
     const bool out = zt == 0.f || zs == 0.f;
     const float w = a.row_weight ? a.row_weight[r] : 1.f;
-    if (threadIdx.x == 0) a.loss[r] = out ? 0.f : w * (gap / zt - logf(zt) + logf(zs));
+    if (lane == 0) a.loss[r] = out ? 0.f : w * (gap / zt - logf(zt) + logf(zs));
     if (!a.d_scores) return;
     float* d = a.d_scores + r * a.n;
-    const float c = w * a.inv_tau, iz = 1.f / zs, izt = 1.f / zt;
-    for (int j = threadIdx.x; j < a.n; j += 128) d[j] = out ? 0.f : c * (expf(s[j] * a.inv_tau - ms) * iz);
-    __syncthreads();
+    const float c = out ? 0.f : w * a.inv_tau, iz = out ? 0.f : 1.f / zs;
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) {
+        const int j = lane + kLanes * k;
+        if (j < a.n) d[j] = c * (v[k] * iz);
+    }
     if (out) return;
-    for (int e = threadIdx.x; e < cnt; e += 128) {
-        const float t = val[a.by_column ? idx[e] : e] * a.inv_tau;
-        const float q = expf(s[idx[e]] * a.inv_tau - ms) * iz;
-        d[idx[e]] = c * (q - (t == -INFINITY ? 0.f : expf(t - mt) * izt));
+    if constexpr (kWarps == 1) __syncwarp();
+    else __syncthreads();
+    const float izt = 1.f / zt;
+    for (int e = lane; e < cnt; e += kLanes) {
+        const int id = idx[e];
+        const float t = val[a.by_column ? id : e], x = __ldg(s + id);
+        const float q = x == -INFINITY ? 0.f : ptx::ex2((x - ms) * c2) * iz;
+        d[id] = c * (q - (t == -INFINITY ? 0.f : ptx::ex2((t - mt) * c2) * izt));
     }
 }
 

@@ -130,6 +130,13 @@ int launch_gemm(const char* what, train::Args a, const DeviceInfo& di, cudaStrea
     return launch_status(what);
 }
 
+template <int kPer, int kWarps>
+int launch_distill(const DistillArgs& a, cudaStream_t s) {
+    const int64_t ctas = kWarps == 1 ? (a.rows + 3) / 4 : a.rows;  // at most 65535 * 16384, under 2^31
+    distill_kernel<kPer, kWarps><<<unsigned(ctas), kWarps == 1 ? 128 : 32 * kWarps, 0, s>>>(a);
+    return launch_status("distill_kernel");
+}
+
 // Query rows of one chunk of the bias gradient's sums: with all heads about two CTAs for each of 148 SMs, but not fewer
 // than eight rows, which a chunk's own start and end cost.
 int bias_chunk_rows(int n, int n_heads) {
@@ -143,18 +150,24 @@ int bias_chunks(int n, int n_heads) {
 
 constexpr int kBiasMaxSmem = 227 * 1024;
 
-template <int kPer>
+template <int kPer, bool kOneSpan>
 int launch_bias_backward(const BiasBackwardArgs& a, int chunks, int n_heads, const DeviceInfo& di, cudaStream_t s) {
     static std::atomic<bool> set[kMaxDevices];
     if (!set[di.ordinal].load()) {
-        cudaError_t e = cudaFuncSetAttribute(bias_backward_kernel<kPer>, cudaFuncAttributeMaxDynamicSharedMemorySize, kBiasMaxSmem);
+        cudaError_t e = cudaFuncSetAttribute(bias_backward_kernel<kPer, kOneSpan>, cudaFuncAttributeMaxDynamicSharedMemorySize, kBiasMaxSmem);
         if (e != cudaSuccess)
             return fail(VEDA_ERR_CUDA, std::string("cudaFuncSetAttribute(bias_backward_kernel): ") + cudaGetErrorString(e));
         set[di.ordinal].store(true);
     }
-    const int threads = std::min(512, std::max(128, (a.n + 31) / 32 * 32));
-    bias_backward_kernel<kPer><<<dim3(chunks, n_heads), threads, (a.offsets + 32) * sizeof(float), s>>>(a);
+    const int threads = std::max(128, ((a.n + kPer - 1) / kPer + 31) / 32 * 32);
+    bias_backward_kernel<kPer, kOneSpan><<<dim3(chunks, n_heads), threads, (a.offsets + 32) * sizeof(float), s>>>(a);
     return launch_status("bias_backward_kernel");
+}
+
+template <int kPer>
+int launch_bias(bool one_span, const BiasBackwardArgs& a, int chunks, int n_heads, const DeviceInfo& di, cudaStream_t s) {
+    return one_span ? launch_bias_backward<kPer, true>(a, chunks, n_heads, di, s)
+                    : launch_bias_backward<kPer, false>(a, chunks, n_heads, di, s);
 }
 
 }  // namespace
@@ -340,11 +353,12 @@ extern "C" int veda_bias_backward(const veda_layout* layout, const float* d_scor
             bias_backward_wide_kernel<<<dim3(chunks, n_heads), 256, smem, s>>>(a);
             rc = launch_status("bias_backward_wide_kernel");
         } else {
-            rc = a.n <= 512    ? launch_bias_backward<1>(a, chunks, n_heads, di, s)
-                 : a.n <= 1024 ? launch_bias_backward<2>(a, chunks, n_heads, di, s)
-                 : a.n <= 2048 ? launch_bias_backward<4>(a, chunks, n_heads, di, s)
-                 : a.n <= 4096 ? launch_bias_backward<8>(a, chunks, n_heads, di, s)
-                               : launch_bias_backward<16>(a, chunks, n_heads, di, s);
+            const bool one = a.n_spans == 1;
+            rc = a.n <= 512    ? launch_bias<1>(one, a, chunks, n_heads, di, s)
+                 : a.n <= 1024 ? launch_bias<2>(one, a, chunks, n_heads, di, s)
+                 : a.n <= 2048 ? launch_bias<4>(one, a, chunks, n_heads, di, s)
+                 : a.n <= 4096 ? launch_bias<8>(one, a, chunks, n_heads, di, s)
+                               : launch_bias<16>(one, a, chunks, n_heads, di, s);
         }
         if (rc) return rc;
         bias_reduce_kernel<<<dim3((a.b.buckets + 255) / 256, n_heads), 256, 0, s>>>(a.partial, d_bias, chunks, a.b.buckets);
@@ -386,8 +400,22 @@ extern "C" int veda_distill(const veda_layout* layout, const float* scores, int3
         a.by_column = by_column;
         a.inv_tau = 1.f / tau;
         a.err = di.err;
-        distill_kernel<<<unsigned(a.rows), 128, 0, static_cast<cudaStream_t>(stream)>>>(a);
-        return launch_status("distill_kernel");
+        cudaStream_t st = static_cast<cudaStream_t>(stream);
+        // 32 columns a thread at most; a warp's own variants in steps of four, so that few loads fall past the row
+        switch (a.n <= 1024 ? (a.n + 127) / 128 : a.n <= 2048 ? 9 : a.n <= 4096 ? 10 : a.n <= 8192 ? 11 : 12) {
+            case 1: return launch_distill<4, 1>(a, st);
+            case 2: return launch_distill<8, 1>(a, st);
+            case 3: return launch_distill<12, 1>(a, st);
+            case 4: return launch_distill<16, 1>(a, st);
+            case 5: return launch_distill<20, 1>(a, st);
+            case 6: return launch_distill<24, 1>(a, st);
+            case 7: return launch_distill<28, 1>(a, st);
+            case 8: return launch_distill<32, 1>(a, st);
+            case 9: return launch_distill<32, 2>(a, st);
+            case 10: return launch_distill<32, 4>(a, st);
+            case 11: return launch_distill<32, 8>(a, st);
+            default: return launch_distill<32, 16>(a, st);
+        }
     });
 }
 
