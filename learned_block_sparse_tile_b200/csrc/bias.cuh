@@ -40,14 +40,15 @@ __host__ __device__ __forceinline__ int bias_bucket(const BiasClasses& b, int dt
     return (it * (2 * b.reach[1] - 1) + ih) * (2 * b.reach[2] - 1) + iw;
 }
 
-// Offsets as one number. In a span of T x H x W tiles a place's number is (t (2H - 1) + h) (2W - 1) + w, and an
+// Offsets as one number. In a span of T x H x W tiles a place's number is (h (2W - 1) + w) (2T - 1) + t, and an
 // offset's number is the difference of two places' numbers, so the bias of a pair is one load of a table per
 // head that holds the bias of every offset: the spans' offsets one span after the other ((2T - 1)(2H - 1)(2W - 1)
 // each, fewer than 8 per tile), then the two buckets of other spans. The layout keeps each tile's part of the
-// index as a key (its number) and as a query (where the table's part of its span is centred, less its number).
+// index as a key (its number) and as a query (where the table's part of its span is centred, less its number). Tiles are
+// in (h, w, t) order, t fastest, and so are the numbers: neighbouring keys read neighbouring entries.
 
-// table[head][o] = bias[head][bucket(o)]
-__global__ void __launch_bounds__(256) bias_expand_kernel(const float* bias, float* table, BiasClasses b,
+// table[head][o] = factor bias[head][bucket(o)]: the sums that start from it are scaled by 1 / factor at their end
+__global__ void __launch_bounds__(256) bias_expand_kernel(const float* bias, float* table, float factor, BiasClasses b,
                                                           const int4* span_grid, int n_spans, int count) {
     const int i = blockIdx.x * 256 + threadIdx.x;
     if (i >= count + 2) return;
@@ -61,10 +62,10 @@ __global__ void __launch_bounds__(256) bias_expand_kernel(const float* bias, flo
             if (o < offsets) break;
             o -= offsets;
         }
-        const int rh = 2 * g.z - 1, rw = 2 * g.w - 1;
-        bucket = bias_bucket(b, o / (rw * rh) - (g.y - 1), (o / rw) % rh - (g.z - 1), o % rw - (g.w - 1));
+        const int rt = 2 * g.y - 1, rw = 2 * g.w - 1;
+        bucket = bias_bucket(b, o % rt - (g.y - 1), o / (rt * rw) - (g.z - 1), (o / rt) % rw - (g.w - 1));
     }
-    table[int64_t(blockIdx.y) * (count + 2) + i] = bias[int64_t(blockIdx.y) * b.buckets + bucket];
+    table[int64_t(blockIdx.y) * (count + 2) + i] = factor * bias[int64_t(blockIdx.y) * b.buckets + bucket];
 }
 
 struct BiasBackwardArgs {
@@ -180,9 +181,9 @@ __global__ void __launch_bounds__(512, kPer <= 4 ? 2 : 1) bias_backward_kernel(c
                 bias_interval(a.b.starts[0], a.b.reach[0], b / (iw * ih), g.y - 1, rt, t0, t1);
                 bias_interval(a.b.starts[1], a.b.reach[1], (b / iw) % ih, g.z - 1, rh, h0, h1);
                 bias_interval(a.b.starts[2], a.b.reach[2], b % iw, g.w - 1, rw, w0, w1);
-                for (int t = t0; t < t1; ++t)
-                    for (int h = h0; h < h1; ++h)
-                        for (int w = w0; w < w1; ++w) sum += at[(t * rh + h) * rw + w];
+                for (int h = h0; h < h1; ++h)
+                    for (int w = w0; w < w1; ++w)
+                        for (int t = t0; t < t1; ++t) sum += at[(h * rw + w) * rt + t];
                 at += rt * rh * rw;
             }
         }

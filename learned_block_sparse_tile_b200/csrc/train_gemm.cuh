@@ -1,30 +1,40 @@
 // fp32 products of the predictor's scores and of their gradients on the tensor cores:
-//     C[batch] = scale A[batch] B[batch]^T (+ a residual, or + the relative position bias),
-// A [M][K] and B [N][K] in any of three layouts in memory, read where they are (no transposed copies).
+//     C[batch][n][m] = scale sum_k A[batch](m, k) B[batch](n, k)  (+ a residual, or + the relative position bias),
+// the operands read where they are, in any of three layouts (no transposed copies).
 //
 // Each fp32 operand is split into two tf32 parts, x = hi + lo, and a b is taken as hi_a hi_b + hi_a lo_b +
-// lo_a hi_b (what is left out is under 1.25 x 2^-20 |a b|; score.cuh has the bound). Two things keep the sums at
-// the level of fp32 rounding as well. The tensor core truncates when it adds into its accumulator, so errors of a
+// lo_a hi_b (what is left out is under 1.25 x 2^-20 |a b|; score.cuh has the bound). What keeps the sums at
+// the level of fp32 rounding as well: the tensor core truncates when it adds into its accumulator, so the errors of a
 // long sum all have one sign and add up (one accumulator over K = 384 and three products loses 1.4e-6, measured;
-// rounded fp32 sums lose 2e-7). So the small products (hi lo and lo hi) have an accumulator of their own, where a
-// truncation is 2^-11 as large, and the sums are cut every kChunk values of K: the epilogue warps add each
-// chunk's two accumulators into registers in rounded fp32.
+// rounded fp32 sums lose 2e-7). So the sums are cut every kChunk values of K, and the epilogue warps add the chunks
+// in registers in rounded fp32; and each slice's small products go first, into an accumulator that is still small.
 //
-// Persistent CTAs walk 128 x 128 output tiles; K runs in slices of 32 (one 128-byte swizzled row per operand row)
-// through a ring of kStages stages, each the hi and lo parts of an A and a B slice:
-//   warp 0       MMA issuer, 12 MMAs per slice; warp 1 owns the TMEM (two buffers of main + correction, 512 columns)
-//   warps 4-11   epilogue, two warps per TMEM lane quarter with half of the columns each: TMEM -> sums in registers ->
-//                global memory, 32 x 32 blocks transposed through shared memory
-//   warps 12-19  producers, two groups that take the slices in turn: global -> registers -> hi and lo in the
-//                swizzled layout, so one group's loads are in flight while the other one splits. A thread's piece
-//                is 16 bytes of one operand row (4 values of K); with K innermost 8 lanes read one row's 128
-//                bytes, with the rows innermost a warp reads 32 neighbouring rows, and either way 8 lanes store
-//                to 8 different 16-byte banks.
-// What bounds it: shared memory. A slice writes 64 KB and its MMAs read 96 KB, about 1250 cycles at 128 bytes per
-// cycle against 768 cycles of tensor time.
+// Both operands need the split, and it is shared memory that bounds the kernel (with both parts of both operands in
+// shared memory an MMA of 128 x 128 x 8 takes 117 cycles instead of 64, measured). So A, whose row a thread can hold, goes
+// to tensor memory straight from its registers, and only B is laid down in shared memory. The products are written
+// so that A's rows are innermost in memory (a warp reads 32 neighbouring rows at one k), which also makes the
+// lanes of an accumulator neighbours in C: the epilogue stores whole 128-byte lines without a transpose.
+//
+// Persistent CTAs walk 128 x 128 tiles; K runs in slices of 32:
+//   warp 0       MMA issuer, 12 MMAs per slice; warp 1 owns the TMEM: the sums twice (columns 0-255) and kStages
+//                stages of A's hi and lo parts (256-511)
+//   warp 2       TMA producer: raw slices of both operands into the split groups' stages
+//   warps 4-11   epilogue, two warps per lane quarter with half of the columns each; their sums start from what is added
+//                to the product, whose loads pass while the tile is computed
+//   warps 12-23  split, three groups with a stage each that take the slices in turn, so that one group's waits pass while
+//                others work. Thread i of 128 has row i of both operands: it reads its 32 values of K (rows of K lie in
+//                the 128-byte swizzle, so that 8 lanes' 16-byte pieces fall into 8 different banks; columns are
+//                neighbours for neighbouring lanes), and writes A's parts to its TMEM lane and B's in the swizzle that
+//                the MMA reads.
+// A score gradient whose row length is no multiple of 16 bytes has no tensor map: the split warps copy its slices themselves,
+// a turn ahead. Each warp copies what its own lanes read, 32 pieces of 32 values, from the 16-byte boundary before each
+// piece (up to three values early and late, inside the tensor), and reads them at the remainder. The tensor's last one
+// to three values, when they fill no 16 bytes, are read from global memory. (The gradient of 819-tile scores took 275 us
+// with values copied one by one, 340 with a bulk copy per piece, 154 with the copies in warps of their own.)
 // Every wait is bounded; a CTA that gives up lets its MMAs finish, frees its TMEM and returns.
 #pragma once
 
+#include <cuda.h>
 #include <cuda_runtime.h>
 
 #include <cstdint>
@@ -36,32 +46,37 @@
 namespace veda {
 namespace train {
 
-constexpr int kBM = 128, kBN = 128, kBK = 32, kChunk = 128;
-constexpr int kPart = 128 * kBK * 4;    // 16 KB: one 128-row slice of one operand part
-constexpr int kStages = 2;
-constexpr int kStageBytes = 4 * kPart;  // A hi, A lo, B hi, B lo
-constexpr int kOffEpi = kStages * kStageBytes;
-constexpr int kEpiBytes = 8 * 16 * 33 * 4;  // a 16 x 33 transpose block per epilogue warp
-constexpr int kOffBar = kOffEpi + kEpiBytes;
-constexpr int kThreads = 640;
+constexpr int kBM = 128, kBN = 128, kBK = 32, kChunk = 64;
+constexpr int kPart = 128 * kBK * 4;    // 16 KB: one 128-row slice of an operand, raw or one part of it
+constexpr int kStageBytes = 2 * kPart;  // B hi, B lo
+constexpr int kStages = 3;              // of the raw slices (A, B) and of their parts; a split group has one of each
+constexpr int kPitch = 36;              // floats a copied piece of 32 values may take
+constexpr int kRawB = 128 * kPitch * 4; // 18 KB: 32 pieces for each of a group's four warps (a tensor-map slice takes less)
+constexpr int kRawBytes = kPart + kRawB;  // A, B
+constexpr int kOffRaw = kStages * kStageBytes;
+constexpr int kOffBar = kOffRaw + kStages * kRawBytes;
+static_assert(kRawBytes % 1024 == 0, "raw slices lie in whole swizzle atoms");
+constexpr int kThreads = 768;
 constexpr int kEpilogue = 256;   // threads
-constexpr int kGroup = 128;      // threads of one producer group
+constexpr int kGroup = 128;      // threads of one split group; as many groups as stages
+constexpr uint32_t kStageA = 256;  // TMEM column of the first stage
 constexpr int kTimeoutBit = 1;
 constexpr uint64_t kDrainNs = 200000000ull;
 
 struct Bars {
-    uint64_t full[kStages];   // producers (one arrival per warp) -> MMA
-    uint64_t empty[kStages];  // MMA commit -> producers
-    uint64_t acc_full[2];     // MMA commit -> epilogue
-    uint64_t acc_empty[2];    // epilogue (one arrival per thread) -> MMA
+    uint64_t raw_full[kStages];   // TMA -> split (transaction bytes)
+    uint64_t raw_empty[kStages];  // split (one arrival per warp) -> TMA
+    uint64_t full[kStages];    // split (one arrival per warp) -> MMA
+    uint64_t empty[kStages];   // MMA commit -> split
+    uint64_t acc_full[2];      // MMA commit -> epilogue
+    uint64_t acc_empty[2];     // epilogue (one arrival per thread) -> MMA
     uint64_t drain;
 };
 constexpr size_t kSmem = 1024 + size_t(kOffBar) + sizeof(Bars) + 16;
 
 enum Layout : int {
-    kRowsVec = 0,  // element (r, k) at r * stride + k, rows of whole 16-byte pieces
-    kRows = 1,     // the same without the alignment
-    kCols = 2,     // element (r, k) at k * stride + r
+    kRows = 0,  // element (r, k) at r * stride + k
+    kCols = 1,  // element (r, k) at k * stride + r
 };
 
 struct Operand {
@@ -70,26 +85,31 @@ struct Operand {
     int64_t stride;
     int rows;
     int layout;
+    int tma;         // 0: no tensor map, copied in pieces (B only, and of all sets or none)
+};
+
+struct Maps {
+    CUtensorMap a[2], b[2];  // boxes of 32 K x 128 rows, 128-byte swizzle (kRows), or 128 rows x 32 K (kCols)
 };
 
 struct Set {
     Operand a, b;
-    float* C;                // [batch][M][N]
-    const float* residual;   // element (m, n) at batch * residual_batch + m * residual_stride + n, or null
-    int64_t residual_batch, residual_stride;
+    float* C;               // [batch][N][M]
+    const float* residual;  // element (n, m) at batch * residual_batch + n * residual_stride + m, or null
 };
 
 struct Args {
     Set set[2];
-    int n_sets, nb;          // operand sets (1 or 2) of one shape, batches in each
+    int n_sets, nb;         // operand sets (1 or 2) of one shape, batches in each
     int M, N, K;
     int tiles_m, tiles_n, n_tiles;
     float scale;
-    // the bias of score tiles (table null: none): table[batch][key number + query number], bias.cuh
+    int64_t residual_batch, residual_stride;
+    // the bias of score tiles (table null: none), m the key and n the query: scale table[batch][key number + query number]
     const float* table;
     const int4* tile_num;
     int64_t table_stride;
-    int offsets;
+    int offsets, one_span;
     uint64_t timeout_ns;
     int* err;
 };
@@ -106,81 +126,106 @@ struct Tile {
     }
 };
 
-// Loads that stay where they are written: the compiler may otherwise move them behind the wait for a free stage, and
-// then nothing hides their latency.
+// Loads that stay where they are written, ahead of the waits that hide their latency.
 __device__ __forceinline__ float load1(const float* p) {
     float v;
     asm volatile("ld.global.nc.f32 %0, [%1];" : "=f"(v) : "l"(p));
     return v;
 }
-__device__ __forceinline__ float4 load4(const float* p) {
-    float4 v;
-    asm volatile("ld.global.nc.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "l"(p));
-    return v;
+
+// sixteen bytes global -> shared in the background
+__device__ __forceinline__ void copy16(uint32_t dst, const float* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 
-// One operand as a producer thread (i of 128) reads it: eight 16-byte pieces of each slice. With kCols piece u is row i,
-// values of K from 4 u; else it is row i / 8 + 16 u, values of K from 4 (i % 8).
-struct Reader {
-    const float* p;    // this thread's first value of slice 0
-    uint32_t stride;
-    int rows;          // rows of the tile from this thread's first one on
-    int layout;
-    bool inside;       // the whole tile's rows exist
-    __device__ __forceinline__ Reader(const Operand& o, int batch, int r0, int i) {
-        layout = o.layout;
-        stride = uint32_t(o.stride);
-        const int r = r0 + (layout == kCols ? i : i >> 3);
-        rows = o.rows - r;
-        inside = r0 + 128 <= o.rows;
-        p = o.base + batch * o.batch + (layout == kCols ? int64_t(r) : int64_t(r) * o.stride + 4 * (i & 7));
+// A warp's pieces of a slice of an operand without a tensor map, as element numbers in the whole tensor (of `total`): its 32
+// rows (kRows), or its 32 columns of every k (kCols).
+struct Pieces {
+    int64_t first;   // element of (the warp's first row, k0)
+    int64_t total;
+    int64_t step;    // between pieces: a row, or a k
+    __device__ __forceinline__ Pieces(const Operand& o, int batch, int r0, int k0, int nb) {
+        first = batch * o.batch + (o.layout == kCols ? int64_t(k0) * o.stride + r0 : int64_t(r0) * o.stride + k0);
+        total = nb * o.batch;
+        step = o.stride;
     }
-    __device__ __forceinline__ void load(float (&v)[32], int k0, int K, int i) const {
-        const bool full = inside && k0 + kBK <= K;
-        if (layout == kCols) {
-            const float* q = p + int64_t(k0) * stride;
-            if (full) {
+    // The warp copies 32 pieces of nine 16-byte parts: eight parts of four pieces at a time, then the ninth of all (needed
+    // only where a piece starts past its boundary). Parts that are not whole inside the tensor are left out; pieces past
+    // the operand's rows or K hold other values of the tensor, which nothing uses.
+    __device__ __forceinline__ void copy(uint32_t dst, const float* base, int lane) const {
+        const int64_t whole = total & ~int64_t(3);
+        int64_t e = first + (lane >> 3) * step;
+        dst += 4 * ((lane >> 3) * kPitch + 4 * (lane & 7));
 #pragma unroll
-                for (int x = 0; x < 32; ++x) v[x] = load1(q + uint32_t(x) * stride);
-            } else {
-                const int ks = rows > 0 ? K - k0 : 0;
-#pragma unroll
-                for (int x = 0; x < 32; ++x) v[x] = x < ks ? load1(q + uint32_t(x) * stride) : 0.f;
-            }
-        } else if (layout == kRowsVec) {
-            const float* q = p + k0;
-#pragma unroll
-            for (int u = 0; u < 8; ++u) {
-                float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
-                if (full || (16 * u < rows && k0 + 4 * (i & 7) < K)) f = load4(q + 16 * u * stride);
-                v[4 * u] = f.x;
-                v[4 * u + 1] = f.y;
-                v[4 * u + 2] = f.z;
-                v[4 * u + 3] = f.w;
-            }
-        } else {
-            const float* q = p + k0;
-            const int ks = K - k0 - 4 * (i & 7);
-#pragma unroll
-            for (int u = 0; u < 8; ++u)
-#pragma unroll
-                for (int x = 0; x < 4; ++x)
-                    v[4 * u + x] = full || (16 * u < rows && x < ks) ? load1(q + 16 * u * stride + x) : 0.f;
+        for (int j = 0; j < 8; ++j) {
+            const int64_t at = (e & ~int64_t(3)) + 4 * (lane & 7);
+            if (at < whole) copy16(dst + 16 * j * kPitch, base + at);
+            e += 4 * step;
         }
+        e = first + lane * step;
+        const int64_t at = (e & ~int64_t(3)) + 32;
+        if ((e & 3) && at < whole) copy16(dst - 4 * ((lane >> 3) * kPitch + 4 * (lane & 7)) + 4 * (lane * kPitch + 32), base + at);
     }
 };
+
+// Half h of this thread's row of a raw slice (row i, K from 16 h).
+__device__ __forceinline__ void read_raw(float (&v)[16], const uint8_t* raw, int layout, int h, int i) {
+    if (layout == kCols) {
+        const float* p = reinterpret_cast<const float*>(raw) + 2048 * h + i;
+#pragma unroll
+        for (int x = 0; x < 16; ++x) v[x] = p[128 * x];
+    } else {
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const float4 f = *reinterpret_cast<const float4*>(raw + i * 128 + (((4 * h + u) ^ (i & 7)) << 4));
+            v[4 * u] = f.x;
+            v[4 * u + 1] = f.y;
+            v[4 * u + 2] = f.z;
+            v[4 * u + 3] = f.w;
+        }
+    }
+}
+
+// The same of a slice that came in pieces: values from K on are zero (A's are too, but what lies there may be NaN).
+__device__ __forceinline__ void read_pieces(float (&v)[16], const uint8_t* raw, const Operand& o, const Pieces& p, int ks, int h, int lane) {
+    const float* q = reinterpret_cast<const float*>(raw);
+    const int64_t whole = p.total & ~int64_t(3);
+    if (o.layout == kCols) {
+        const int64_t e = p.first + lane + 16 * h * p.step;   // this thread's first value
+        const uint32_t at = uint32_t(p.first + 16 * h * p.step), step = uint32_t(p.step);
+#pragma unroll
+        for (int x = 0; x < 16; ++x) v[x] = q[(16 * h + x) * kPitch + ((at + x * step) & 3) + lane];
+        if (16 * h + 16 > ks || e + 15 * p.step >= whole) {
+#pragma unroll
+            for (int x = 0; x < 16; ++x) {
+                if (16 * h + x >= ks) v[x] = 0.f;
+                else if (e + x * p.step >= whole) v[x] = e + x * p.step < p.total ? load1(o.base + e + x * p.step) : 0.f;
+            }
+        }
+    } else {
+        const int64_t e = p.first + lane * p.step;
+        const float* r = q + lane * kPitch + (uint32_t(e) & 3) + 16 * h;
+#pragma unroll
+        for (int x = 0; x < 16; ++x) v[x] = r[x];
+        if (16 * h + 16 > ks || e + 16 * h + 15 >= whole) {
+#pragma unroll
+            for (int x = 0; x < 16; ++x) {
+                if (16 * h + x >= ks) v[x] = 0.f;
+                else if (e + 16 * h + x >= whole) v[x] = e + 16 * h + x < p.total ? load1(o.base + e + 16 * h + x) : 0.f;
+            }
+        }
+    }
+}
 
 // x rounded to the nearest tf32 value, ties away from zero; infinities stay, a NaN's remainder stays NaN
 __device__ __forceinline__ float hi_part(float x) { return __uint_as_float((__float_as_uint(x) + 0x1000u) & 0xffffe000u); }
 
-// the pieces as hi and lo parts in the 128-byte swizzle (16-byte piece c of row r at piece c ^ (r % 8))
-__device__ __forceinline__ void store_slice(const float (&v)[32], uint8_t* part, int layout, int i) {
-    const bool cols = layout == kCols;
-    // piece u of a row's eight lies at c ^ (r % 8): r is fixed with kCols, c with the others, and r % 8 = (i / 8) % 8 there
-    uint8_t* row = part + (cols ? i * 128 : (i >> 3) * 128 + (((i & 7) ^ ((i >> 3) & 7)) << 4));
+// Half `half` of B's values of this thread's row as hi and lo parts in the 128-byte swizzle (16-byte piece c of row r at
+// piece c ^ (r % 8))
+__device__ __forceinline__ void store_b(const float (&v)[16], uint8_t* part, int half, int i) {
 #pragma unroll
-    for (int u = 0; u < 8; ++u) {
-        uint8_t* dst = cols ? row + ((u ^ (i & 7)) << 4) : row + u * 2048;
+    for (int u = 0; u < 4; ++u) {
+        uint8_t* dst = part + i * 128 + (((4 * half + u) ^ (i & 7)) << 4);
         float4 h, l;
         h.x = hi_part(v[4 * u]);
         h.y = hi_part(v[4 * u + 1]);
@@ -195,7 +240,38 @@ __device__ __forceinline__ void store_slice(const float (&v)[32], uint8_t* part,
     }
 }
 
-__global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant__ Args a) {
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const float (&r)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+        "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
+        "f"(r[0]), "f"(r[1]), "f"(r[2]), "f"(r[3]), "f"(r[4]), "f"(r[5]), "f"(r[6]), "f"(r[7]), "f"(r[8]), "f"(r[9]),
+        "f"(r[10]), "f"(r[11]), "f"(r[12]), "f"(r[13]), "f"(r[14]), "f"(r[15])
+        : "memory");
+}
+
+// Half of A's values of this thread's row (its TMEM lane): hi parts in 16 columns, lo parts 32 columns behind them
+__device__ __forceinline__ void store_a(const float (&v)[16], uint32_t taddr) {
+    float h[16];
+#pragma unroll
+    for (int x = 0; x < 16; ++x) h[x] = hi_part(v[x]);
+    tmem_st16(taddr, h);
+#pragma unroll
+    for (int x = 0; x < 16; ++x) h[x] = v[x] - h[x];
+    tmem_st16(taddr + 32, h);
+}
+
+// D[tmem] (+)= A[tmem] * B[smem desc], kind::tf32: A (M x K) in lanes 0..M-1, one value per column
+__device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t id, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p, e;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::tf32 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(b_desc), "r"(id), "r"(accumulate)
+        : "memory");
+}
+
+__global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Args a) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     Bars& B = *reinterpret_cast<Bars*>(smem + kOffBar);
@@ -207,12 +283,16 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < kStages; ++s) {
+            ptx::mbar_init(&B.raw_full[s], 1);
+            ptx::mbar_init(&B.raw_empty[s], kGroup / 32);
+        }
+        for (int s = 0; s < kStages; ++s) {
             ptx::mbar_init(&B.full[s], kGroup / 32);
             ptx::mbar_init(&B.empty[s], 1);
         }
-        for (int b = 0; b < 2; ++b) {
-            ptx::mbar_init(&B.acc_full[b], 1);
-            ptx::mbar_init(&B.acc_empty[b], kEpilogue);
+        for (int s = 0; s < 2; ++s) {
+            ptx::mbar_init(&B.acc_full[s], 1);
+            ptx::mbar_init(&B.acc_empty[s], kEpilogue);
         }
         ptx::mbar_init(&B.drain, 1);
         *abort_flag = 0;
@@ -224,7 +304,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
     const uint32_t tmem = *tmem_slot;
 
     if (warp < 4) {
-        ptx::regs_dec<40>();
+        ptx::regs_dec<56>();
         if (warp == 0) {
             // ------------------------------------------------------------------------ MMA issuer
             constexpr uint32_t kId = tf32x3::idesc(kBM, kBN);
@@ -232,31 +312,26 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
             bool stop = false;
             for (int t = blockIdx.x; t < a.n_tiles && !stop; t += gridDim.x) {
                 for (int kk = 0; kk < nk; ++kk, ++g) {
-                    const int s = g % kStages, ph = g / kStages, b = gc & 1;
+                    const int s = g % kStages, b = gc & 1;
                     const bool first = kk % (kChunk / kBK) == 0;
-                    if (first && !warp_wait(&B.acc_empty[b], ((gc >> 1) & 1) ^ 1, abort_flag, tmo)) {
-                        stop = true;
-                        break;
-                    }
-                    if (!warp_wait(&B.full[s], ph & 1, abort_flag, tmo)) {
+                    if ((first && !warp_wait(&B.acc_empty[b], ((gc >> 1) & 1) ^ 1, abort_flag, tmo)) ||
+                        !warp_wait(&B.full[s], (g / kStages) & 1, abort_flag, tmo)) {
                         stop = true;
                         break;
                     }
                     ptx::tc_fence_after();
-                    const uint32_t d = tmem + uint32_t(b * 256);
+                    const uint32_t d = tmem + uint32_t(b * 128), ah = tmem + kStageA + uint32_t(s * 64);
                     const uint32_t base = ptx::smem_addr(smem + s * kStageBytes);
-                    const uint64_t ah = ptx::smem_desc_sw128(base, 16, 1024);
-                    const uint64_t al = ptx::smem_desc_sw128(base + kPart, 16, 1024);
-                    const uint64_t bh = ptx::smem_desc_sw128(base + 2 * kPart, 16, 1024);
-                    const uint64_t bl = ptx::smem_desc_sw128(base + 3 * kPart, 16, 1024);
+                    const uint64_t bh = ptx::smem_desc_sw128(base, 16, 1024);
+                    const uint64_t bl = ptx::smem_desc_sw128(base + kPart, 16, 1024);
+                    // 8 tf32 = 32 bytes of B per k-step (2 of the descriptor's 16-byte units), 8 columns of A
 #pragma unroll
                     for (int k8 = 0; k8 < kBK / 8; ++k8) {
-                        const uint64_t o = uint64_t(k8 * 2);  // 8 tf32 = 32 bytes per k-step, in 16-byte units
-                        const uint32_t add = first && k8 == 0 ? 0u : 1u;
-                        tf32x3::mma_ss_w(d, ah + o, bh + o, kId, add);
-                        tf32x3::mma_ss_w(d + 128, al + o, bh + o, kId, add);
-                        tf32x3::mma_ss_w(d + 128, ah + o, bl + o, kId, 1u);
+                        mma_ts(d, ah + 32 + 8 * k8, bh + uint64_t(2 * k8), kId, first && k8 == 0 ? 0u : 1u);
+                        mma_ts(d, ah + 8 * k8, bl + uint64_t(2 * k8), kId, 1u);
                     }
+#pragma unroll
+                    for (int k8 = 0; k8 < kBK / 8; ++k8) mma_ts(d, ah + 8 * k8, bh + uint64_t(2 * k8), kId, 1u);
                     ptx::mma_commit_w(&B.empty[s]);
                     if (kk % (kChunk / kBK) == kChunk / kBK - 1 || kk == nk - 1) {
                         ptx::mma_commit_w(&B.acc_full[b]);
@@ -268,17 +343,90 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
             volatile int never = 0;
             ptx::mma_commit_w(&B.drain);
             ptx::mbar_wait(&B.drain, 0, &never, kDrainNs);
+        } else if (warp == 2) {
+            // ------------------------------------------------------------------------ TMA producer
+            const uint64_t keep = ptx::policy_evict_last();  // operand rows are read by several tiles
+            int g = 0;
+            bool stop = false;
+            for (int t = blockIdx.x; t < a.n_tiles && !stop; t += gridDim.x) {
+                const Tile w(a, t);
+                const int la = w.set ? a.set[1].a.layout : a.set[0].a.layout;
+                const int lb = w.set ? a.set[1].b.layout : a.set[0].b.layout;
+                const int tma_b = w.set ? a.set[1].b.tma : a.set[0].b.tma;
+                const CUtensorMap *ma = w.set ? &maps.a[1] : &maps.a[0], *mb = w.set ? &maps.b[1] : &maps.b[0];
+                for (int kk = 0; kk < nk; ++kk, ++g) {
+                    const int s = g % kStages, ph = g / kStages, k0 = kk * kBK;
+                    if (!warp_wait(&B.raw_empty[s], (ph & 1) ^ 1, abort_flag, tmo)) {
+                        stop = true;
+                        break;
+                    }
+                    if (ptx::elect_one()) {
+                        uint8_t* raw = smem + kOffRaw + s * kRawBytes;
+                        ptx::mbar_arrive_expect_tx(&B.raw_full[s], tma_b ? 2 * kPart : kPart);
+                        ptx::tma_load_3d_hint(raw, ma, la == kCols ? w.m0 : k0, la == kCols ? k0 : w.m0, w.batch,
+                                              &B.raw_full[s], keep);
+                        if (tma_b)
+                            ptx::tma_load_3d_hint(raw + kPart, mb, lb == kCols ? w.n0 : k0, lb == kCols ? k0 : w.n0, w.batch,
+                                                  &B.raw_full[s], keep);
+                    }
+                    __syncwarp();
+                }
+            }
+            if (*abort_flag && lane == 0) {
+                // every copy already issued must land before the CTA releases its shared memory
+                volatile int never = 0;
+                for (int k = (g > kStages ? g - kStages : 0); k < g; ++k)
+                    ptx::mbar_wait(&B.raw_full[k % kStages], (k / kStages) & 1, &never, kDrainNs);
+            }
         }
     } else if (warp < 12) {
         // ---------------------------------------------------------------------------- epilogue
-        ptx::regs_inc<112>();
-        const int q = warp & 3, half = (warp - 4) >> 2;  // TMEM lane quarter (rows 32 q ..), columns 64 half ..
-        float* tr = reinterpret_cast<float*>(smem + kOffEpi) + (warp - 4) * 16 * 33;
+        ptx::regs_inc<88>();
+        const int q = warp & 3, half = (warp - 4) >> 2;  // TMEM lane quarter (m 32 q ..), columns 64 half ..
         int gc = 0;
         bool stop = false;
         for (int t = blockIdx.x; t < a.n_tiles && !stop; t += gridDim.x) {
             const Tile w(a, t);
-            float acc[64];
+            const uint32_t lanes = tmem + (uint32_t(32 * q) << 16) + uint32_t(64 * half);
+            const int m = w.m0 + 32 * q + lane, mm = min(m, a.M - 1), n0 = w.n0 + 64 * half;
+            const int left = a.N - n0;
+            // (selects, not a.set[w.set]: a runtime index into the kernel arguments would copy them to the stack)
+            const float* res = w.set ? a.set[1].residual : a.set[0].residual;
+            float acc[64];  // what is added to the product, over its scale, then the sums; loads from clamped places
+            if (a.table) {
+                const float* table = a.table + w.batch * a.table_stride;
+                const int4 key = a.tile_num[mm];
+#pragma unroll
+                for (int j = 0; j < 64; j += 32) {
+                    const int4 mine = a.tile_num[min(n0 + j + lane, a.N - 1)];
+#pragma unroll
+                    for (int x = 0; x < 32; ++x) {
+                        int o = key.y + __shfl_sync(0xffffffffu, mine.z, x);
+                        if (!a.one_span) {
+                            const int span = __shfl_sync(0xffffffffu, mine.x, x);
+                            if (key.x != span) o = a.offsets + (key.x > span);
+                        }
+                        acc[j + x] = load1(table + o);
+                    }
+                }
+            } else if (res) {
+                res += w.batch * a.residual_batch + mm;
+#pragma unroll
+                for (int x = 0; x < 64; ++x) acc[x] = load1(res + min(n0 + x, a.N - 1) * a.residual_stride);
+            } else {
+#pragma unroll
+                for (int x = 0; x < 64; ++x) acc[x] = 0.f;
+            }
+            const auto add = [&](uint32_t from) {
+#pragma unroll
+                for (int j = 0; j < 64; j += 16) {
+                    uint32_t x[16];
+                    ptx::tmem_ld16(from + j, x);
+                    ptx::tmem_wait_ld();
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) acc[j + e] += __uint_as_float(x[e]);
+                }
+            };
             for (int c = 0; c < nc; ++c, ++gc) {
                 const int b = gc & 1;
                 if (!warp_wait(&B.acc_full[b], (gc >> 1) & 1, abort_flag, tmo)) {
@@ -286,98 +434,96 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
                     break;
                 }
                 ptx::tc_fence_after();
-                const uint32_t taddr = tmem + (uint32_t(32 * q) << 16) + uint32_t(b * 256 + 64 * half);
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    uint32_t x[16], y[16];
-                    ptx::tmem_ld16(taddr + 16 * j, x);
-                    ptx::tmem_ld16(taddr + 128 + 16 * j, y);
-                    ptx::tmem_wait_ld();
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) {
-                        const float v = __uint_as_float(x[e]) + __uint_as_float(y[e]);
-                        acc[16 * j + e] = c == 0 ? v : acc[16 * j + e] + v;
-                    }
-                }
+                add(lanes + uint32_t(b * 128));
                 ptx::tc_fence_before();
                 ptx::mbar_arrive(&B.acc_empty[b]);
             }
             if (stop) break;
-            // (a select, not a.set[w.set]: a runtime index into the kernel arguments would copy them to the stack)
-            float* C = (w.set ? a.set[1].C : a.set[0].C) + int64_t(w.batch) * a.M * a.N;
-            const float* res = w.set ? a.set[1].residual : a.set[0].residual;
-            const int64_t rs = a.set[0].residual_stride;
-            if (res) res += w.batch * a.set[0].residual_batch;
-            const float* table = a.table ? a.table + w.batch * a.table_stride : nullptr;
-            const int row0 = w.m0 + 32 * q;
-            int4 query = make_int4(0, 0, 0, 0);
-            if (table) query = a.tile_num[min(row0 + lane, a.M - 1)];
+            if (m < a.M) {
+                float* C = (w.set ? a.set[1].C : a.set[0].C) + int64_t(w.batch) * a.M * a.N + int64_t(n0) * a.M + m;
+                if (left >= 64) {
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const int n = w.n0 + 64 * half + 32 * j + lane, nn = min(n, a.N - 1);
-                int4 key = make_int4(0, 0, 0, 0);
-                if (table) key = a.tile_num[nn];
-                // sixteen rows at a time: the lanes that hold them lay them down, and what is added to them is loaded
-                // while they do, from clamped places
+                    for (int x = 0; x < 64; ++x) C[uint32_t(x) * uint32_t(a.M)] = acc[x] * a.scale;
+                } else {
 #pragma unroll
-                for (int r16 = 0; r16 < 32; r16 += 16) {
-                    float more[16];
-                    if (table) {
-#pragma unroll
-                        for (int x = 0; x < 16; ++x) {
-                            const int span = __shfl_sync(0xffffffffu, query.x, r16 + x);
-                            const int num = __shfl_sync(0xffffffffu, query.z, r16 + x);
-                            more[x] = __ldg(table + (key.x != span ? a.offsets + (key.x > span) : key.y + num));
-                        }
-                    } else if (res) {
-#pragma unroll
-                        for (int x = 0; x < 16; ++x) more[x] = __ldg(res + min(row0 + r16 + x, a.M - 1) * rs + nn);
-                    } else {
-#pragma unroll
-                        for (int x = 0; x < 16; ++x) more[x] = 0.f;
-                    }
-                    if ((lane & 16) == r16) {
-#pragma unroll
-                        for (int e = 0; e < 32; ++e) tr[(lane & 15) * 33 + e] = acc[32 * j + e];
-                    }
-                    __syncwarp();
-                    float* dst = C + int64_t(row0 + r16) * a.N + n;
-#pragma unroll
-                    for (int x = 0; x < 16; ++x) {
-                        const float v = tr[x * 33 + lane] * a.scale + more[x];
-                        if (row0 + r16 + x < a.M && n < a.N) dst[int64_t(x) * a.N] = v;
-                    }
-                    __syncwarp();
+                    for (int x = 0; x < 64; ++x)
+                        if (x < left) C[uint32_t(x) * uint32_t(a.M)] = acc[x] * a.scale;
                 }
             }
         }
     } else {
-        // ---------------------------------------------------------------------------- producers
-        ptx::regs_inc<104>();
-        const int i = threadIdx.x & (kGroup - 1), group = (warp - 12) >> 2;
-        int g = 0;  // slices of the tiles before this one; a group takes every second slice of the CTA's sequence
-        bool stop = false;
-        for (int t = blockIdx.x; t < a.n_tiles && !stop; t += gridDim.x, g += nk) {
-            const Tile w(a, t);
-            const Reader ra(w.set ? a.set[1].a : a.set[0].a, w.batch, w.m0, i);
-            const Reader rb(w.set ? a.set[1].b : a.set[0].b, w.batch, w.n0, i);
-            for (int kk = (group ^ g) & 1; kk < nk; kk += 2) {
-                float va[32], vb[32];
-                ra.load(va, kk * kBK, a.K, i);
-                rb.load(vb, kk * kBK, a.K, i);
-                const int s = (g + kk) % kStages, ph = (g + kk) / kStages;
-                if (!warp_wait(&B.empty[s], (ph & 1) ^ 1, abort_flag, tmo)) {
-                    stop = true;
-                    break;
-                }
-                uint8_t* st = smem + s * kStageBytes;
-                store_slice(va, st, ra.layout, i);
-                store_slice(vb, st + 2 * kPart, rb.layout, i);
-                tf32x3::fence_async_smem();
-                __syncwarp();
-                if (lane == 0) ptx::mbar_arrive(&B.full[s]);
-            }
+        // ---------------------------------------------------------------------------- split
+        ptx::regs_dec<80>();
+        const int s = (warp - 12) >> 2, i = threadIdx.x & (kGroup - 1);  // the group's number is its stage's
+        const uint32_t stage_a = tmem + kStageA + uint32_t(64 * s) + (uint32_t(32 * (warp & 3)) << 16);
+        uint8_t* stage_b = smem + s * kStageBytes;
+        const uint8_t* raw = smem + kOffRaw + s * kRawBytes;
+        const bool pieces = !a.set[0].b.tma;
+        uint8_t* my_raw = smem + kOffRaw + s * kRawBytes + kPart + (warp & 3) * 32 * kPitch * 4;
+        // this group's slices, every kStages-th of the CTA's sequence: tile t, slice kk, number `use` of the group
+        int t = blockIdx.x, kk = s, use = 0;
+        while (kk >= nk && t < a.n_tiles) {
+            kk -= nk;
+            t += gridDim.x;
         }
+        const auto copy_b = [&](int t, int kk) {
+            const Tile w(a, t);
+            const Operand& o = w.set ? a.set[1].b : a.set[0].b;
+            Pieces(o, w.batch, w.n0 + (i & 96), kk * kBK, a.nb).copy(ptx::smem_addr(my_raw), o.base, lane);
+        };
+        if (pieces && t < a.n_tiles) copy_b(t, kk);
+        Tile w(a, t);
+        while (t < a.n_tiles) {
+            const Operand& ob = w.set ? a.set[1].b : a.set[0].b;
+            const int la = w.set ? a.set[1].a.layout : a.set[0].a.layout;
+            int next = t, next_kk = kk + kStages;
+            while (next_kk >= nk && next < a.n_tiles) {
+                next_kk -= nk;
+                next += gridDim.x;
+            }
+            if (!warp_wait(&B.raw_full[s], use & 1, abort_flag, tmo) ||
+                !warp_wait(&B.empty[s], (use & 1) ^ 1, abort_flag, tmo))
+                break;
+            ptx::tc_fence_after();
+            if (pieces) {
+                asm volatile("cp.async.wait_all;" ::: "memory");
+                __syncwarp();
+                const Pieces p(ob, w.batch, w.n0 + (i & 96), kk * kBK, a.nb);
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    float v[16];
+                    read_pieces(v, my_raw, ob, p, a.K - kk * kBK, h, lane);
+                    store_b(v, stage_b, h, i);
+                }
+                __syncwarp();  // every lane has read the pieces
+                if (next < a.n_tiles) copy_b(next, next_kk);
+            } else {
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    float v[16];
+                    read_raw(v, raw + kPart, ob.layout, h, i);
+                    store_b(v, stage_b, h, i);
+                }
+            }
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                float v[16];
+                read_raw(v, raw, la, h, i);
+                store_a(v, stage_a + 16 * h);
+            }
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(&B.raw_empty[s]);
+            tf32x3::fence_async_smem();
+            ptx::tmem_wait_st();
+            ptx::tc_fence_before();
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(&B.full[s]);
+            if (next != t) w = Tile(a, next);
+            t = next;
+            kk = next_kk;
+            ++use;
+        }
+        asm volatile("cp.async.wait_all;" ::: "memory");
     }
 
     __syncthreads();

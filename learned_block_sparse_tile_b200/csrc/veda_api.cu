@@ -435,6 +435,21 @@ int make_f32_map(CUtensorMap* m, const float* base, int64_t K, int64_t rows, int
     return VEDA_OK;
 }
 
+int make_f32_cols_map(CUtensorMap* m, const float* base, int64_t rows, int64_t K, int64_t batch) {
+    auto enc = tensor_map_encoder();
+    if (!enc) return fail(VEDA_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
+    cuuint64_t gdim[3] = {cuuint64_t(rows), cuuint64_t(K), cuuint64_t(batch)};
+    cuuint64_t gstride[2] = {cuuint64_t(rows) * 4, cuuint64_t(rows) * cuuint64_t(K) * 4};
+    cuuint32_t box[3] = {128, 32, 1};
+    cuuint32_t estride[3] = {1, 1, 1};
+    CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, const_cast<float*>(base), gdim, gstride, box, estride,
+                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS)
+        return fail(VEDA_ERR_CUDA, "cuTensorMapEncodeTiled (fp32 columns) failed (" + std::to_string(int(r)) + ")");
+    return VEDA_OK;
+}
+
 int launch_score_gemms(const float* feats_q, const float* feats_k, const float* proj_q, const float* proj_k, float* qh,
                        float* kh, float* pt_q, float* pt_k, float* scores, int nv, int dim, int n_heads,
                        cudaStream_t s) {

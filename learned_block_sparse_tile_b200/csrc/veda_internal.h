@@ -53,6 +53,10 @@ int current_device(DeviceInfo* out);
 // Device copy of a layout's index data on the current device (made on first use).
 int layout_on_device(const veda_layout* lay, const DeviceCopy** out);
 uint64_t wait_timeout_ns();
+// TMA map over fp32 [batch][rows][K] (K innermost): boxes of 32 K x 128 rows with the 128-byte swizzle
+int make_f32_map(CUtensorMap* m, const float* base, int64_t K, int64_t rows, int64_t batch);
+// the same over [batch][K][rows] (rows innermost): boxes of 128 rows x 32 K, not swizzled
+int make_f32_cols_map(CUtensorMap* m, const float* base, int64_t rows, int64_t K, int64_t batch);
 // TMA map over bf16 rows [rows, dim] in boxes of 128 rows x 64 columns with the 128-byte swizzle
 int make_bf16_rows_map(CUtensorMap* m, const void* base, int64_t rows, int dim);
 // `cudaGetLastError` after a launch, as a VEDA_* status

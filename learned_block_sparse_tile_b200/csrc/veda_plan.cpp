@@ -206,16 +206,16 @@ extern "C" int veda_plan(const veda_span* spans, int32_t n_spans, int64_t seq_le
         for (int a = 0; a < 3; ++a) tiles[a] = int32_t(round_up(s.grid[a], s.box[a]) / s.box[a]);
         lay->span_grid.insert(lay->span_grid.end(),
                               {int32_t(before / veda::kTile), tiles[0], tiles[1], tiles[2]});
-        const int32_t rh = 2 * tiles[1] - 1, rw = 2 * tiles[2] - 1;
-        const int32_t centre = lay->bias_offsets + ((tiles[0] - 1) * rh + tiles[1] - 1) * rw + tiles[2] - 1;
+        const int32_t rt = 2 * tiles[0] - 1, rw = 2 * tiles[2] - 1;
+        const int32_t centre = lay->bias_offsets + ((tiles[1] - 1) * rw + tiles[2] - 1) * rt + tiles[0] - 1;
         for (int32_t bh = 0; bh < tiles[1]; ++bh)
             for (int32_t bw = 0; bw < tiles[2]; ++bw)
                 for (int32_t bt = 0; bt < tiles[0]; ++bt) {
-                    const int32_t num = (bt * rh + bh) * rw + bw;
+                    const int32_t num = (bh * rw + bw) * rt + bt;
                     lay->tile_pos.insert(lay->tile_pos.end(), {int32_t(i), bt, bh, bw});
                     lay->tile_num.insert(lay->tile_num.end(), {int32_t(i), num, centre - num, 0});
                 }
-        lay->bias_offsets += (2 * tiles[0] - 1) * rh * rw;
+        lay->bias_offsets += (2 * tiles[1] - 1) * rw * rt;
         if (i + 1 < use.size()) {
             ref_tiles += int64_t(perm.size() - before) / veda::kTile;
             ref_tokens += rows;

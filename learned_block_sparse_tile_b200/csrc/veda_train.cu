@@ -106,9 +106,15 @@ int launch_teacher(const teacher::Maps& m, const teacher::Args& a, const DeviceI
     return launch_status("teacher_kernel");
 }
 
-train::Operand operand(const float* base, int64_t batch, int64_t stride, int rows, bool cols) {
-    const bool whole = stride % 4 == 0 && batch % 4 == 0;
-    return {base, batch, stride, rows, cols ? train::kCols : whole ? train::kRowsVec : train::kRows};
+// [batch][rows][K] with rows of K innermost (cols: [batch][K][rows]), densely packed
+train::Operand operand(const float* base, int rows, int K, bool cols) {
+    const int64_t stride = cols ? rows : K;
+    return {base, int64_t(rows) * K, stride, rows, cols ? train::kCols : train::kRows, stride % 4 == 0};
+}
+
+int operand_map(CUtensorMap* m, const train::Operand& o, int K, int batches) {
+    if (!o.tma) return VEDA_OK;
+    return o.layout == train::kCols ? make_f32_cols_map(m, o.base, o.rows, K, batches) : make_f32_map(m, o.base, K, o.rows, batches);
 }
 
 int launch_gemm(const char* what, train::Args a, const DeviceInfo& di, cudaStream_t s) {
@@ -126,7 +132,12 @@ int launch_gemm(const char* what, train::Args a, const DeviceInfo& di, cudaStrea
     a.n_tiles = int(tiles);
     a.timeout_ns = wait_timeout_ns();
     a.err = di.err;
-    train::gemm_kernel<<<unsigned(std::min(a.n_tiles, di.sms)), train::kThreads, train::kSmem, s>>>(a);
+    train::Maps m{};
+    for (int i = 0; i < a.n_sets; ++i) {
+        if (int rc = operand_map(&m.a[i], a.set[i].a, a.K, a.nb)) return rc;
+        if (int rc = operand_map(&m.b[i], a.set[i].b, a.K, a.nb)) return rc;
+    }
+    train::gemm_kernel<<<unsigned(std::min(a.n_tiles, di.sms)), train::kThreads, train::kSmem, s>>>(m, a);
     return launch_status(what);
 }
 
@@ -276,22 +287,24 @@ extern "C" int veda_score_bias(const veda_layout* layout, const float* feats_q, 
         float* table = static_cast<float*>(workspace);
         if (bias) {
             bias_expand_kernel<<<dim3((offsets + 2 + 255) / 256, n_heads), 256, 0, s>>>(
-                bias, table, b, reinterpret_cast<const int4*>(dc->span_grid), int(layout->span_grid.size() / 4), offsets);
+                bias, table, float(std::sqrt(double(dim))), b, reinterpret_cast<const int4*>(dc->span_grid), int(layout->span_grid.size() / 4), offsets);
             if (int rc = launch_status("bias_expand_kernel")) return rc;
         }
         const int64_t nf = int64_t(n) * 3 * dim, nd = int64_t(n) * dim;
+        // hats[tile][d], both sides in one launch, then scores[query][key]
         train::Args p{};
         p.n_sets = 2;
         p.nb = n_heads;
-        p.M = n;
-        p.N = dim;
+        p.M = dim;
+        p.N = n;
         p.K = 3 * dim;
         p.scale = 1.f;
+        p.residual_batch = nf;
+        p.residual_stride = 3 * dim;
         for (int side = 0; side < 2; ++side) {
             const float* f = side ? feats_k : feats_q;
-            p.set[side] = {operand(f, nf, 3 * dim, n, false),
-                           operand(side ? proj_k : proj_q, 3 * int64_t(dim) * dim, dim, dim, true),
-                           hats + side * n_heads * nd, f, nf, 3 * dim};
+            p.set[side] = {operand(side ? proj_k : proj_q, dim, 3 * dim, true), operand(f, n, 3 * dim, false),
+                           hats + side * n_heads * nd, f};
         }
         if (int rc = launch_gemm("veda_score_bias (projections)", p, di, s)) return rc;
         train::Args l{};
@@ -300,7 +313,8 @@ extern "C" int veda_score_bias(const veda_layout* layout, const float* feats_q, 
         l.M = l.N = n;
         l.K = dim;
         l.scale = float(1.0 / std::sqrt(double(dim)));
-        l.set[0] = {operand(hats, nd, dim, n, false), operand(hats + n_heads * nd, nd, dim, n, false), scores, nullptr, 0, 0};
+        l.set[0] = {operand(hats + n_heads * nd, n, dim, false), operand(hats, n, dim, false), scores, nullptr};
+        l.one_span = layout->span_grid.size() == 4;
         if (bias) l.table = table;
         l.tile_num = reinterpret_cast<const int4*>(dc->tile_num);
         l.table_stride = offsets + 2;
@@ -441,24 +455,25 @@ extern "C" int veda_score_backward(const veda_layout* layout, const float* feats
         DeviceInfo di;
         if (int rc = current_device(&di)) return rc;
         const int n = layout->desc.n_video;
-        const int64_t nf = int64_t(n) * 3 * dim, nd = int64_t(n) * dim, nn = int64_t(n) * n;
+        const int64_t nd = int64_t(n) * dim;
         float* dx = static_cast<float*>(workspace);
         cudaStream_t s = static_cast<cudaStream_t>(stream);
         const float c = float(1.0 / std::sqrt(double(dim)));
-        // dq_hat = c dS k_hat and dk_hat = c dS^T q_hat, then dP = feats^T dx_hat, both sides in one launch
+        // dq_hat[i][d] = c sum_j dS[i][j] k_hat[j][d] and dk_hat[j][d] = c sum_i dS[i][j] q_hat[i][d], then
+        // dP[f][d] = sum_i feats[i][f] dx_hat[i][d]; both sides in one launch
         train::Args x{}, p{};
         x.n_sets = p.n_sets = 2;
         x.nb = p.nb = n_heads;
-        x.M = x.K = p.K = n;
-        x.N = p.N = dim;
-        p.M = 3 * dim;
+        x.M = p.M = dim;
+        x.N = x.K = p.K = n;
+        p.N = 3 * dim;
         x.scale = c;
         p.scale = 1.f;
         for (int side = 0; side < 2; ++side) {
-            x.set[side] = {operand(d_scores, nn, n, n, side == 1), operand(hats + (side ? 0 : n_heads * nd), nd, dim, dim, true),
-                           dx + side * n_heads * nd, nullptr, 0, 0};
-            p.set[side] = {operand(side ? feats_k : feats_q, nf, 3 * dim, 3 * dim, true),
-                           operand(dx + side * n_heads * nd, nd, dim, dim, true), side ? d_proj_k : d_proj_q, nullptr, 0, 0};
+            x.set[side] = {operand(hats + (side ? 0 : n_heads * nd), dim, n, true), operand(d_scores, n, n, side == 1),
+                           dx + side * n_heads * nd, nullptr};
+            p.set[side] = {operand(dx + side * n_heads * nd, dim, n, true), operand(side ? feats_k : feats_q, 3 * dim, n, true),
+                           side ? d_proj_k : d_proj_q, nullptr};
         }
         if (int rc = launch_gemm("veda_score_backward (projected features)", x, di, s)) return rc;
         return launch_gemm("veda_score_backward (projections)", p, di, s);

@@ -8,12 +8,14 @@
 namespace veda {
 
 // As ptx::mbar_wait (false when `*abort` is raised or after `timeout_ns`, raising it then), but the clock is first
-// read after a number of try_waits, each of which the hardware suspends for a while: reading the global timer on
-// every wait that does not pass at once costs more than the wait itself.
+// read after a number of tries, each of which sleeps until the phase completes or its hint runs out: reading the global
+// timer on every wait that does not pass at once costs more than the wait itself, and tries without a hint come back
+// at once and take issue slots from the warps that work.
 __device__ __forceinline__ bool bounded_wait(uint64_t* bar, uint32_t parity, volatile int* abort, uint64_t timeout_ns) {
+    if (ptx::mbar_try_wait(bar, parity)) return true;
 #pragma unroll 1
-    for (int i = 0; i < 64; ++i)
-        if (ptx::mbar_try_wait(bar, parity)) return true;
+    for (int i = 0; i < 8; ++i)
+        if (ptx::mbar_try_wait_sleep(bar, parity, 20000u)) return true;
     return ptx::mbar_wait(bar, parity, abort, timeout_ns);
 }
 
