@@ -416,7 +416,19 @@ def _need(who, device, *tensors):
 def _workspace(who, device, t):
     if not t.is_contiguous() or t.get_device() != device:
         raise VedaError(VEDA_ERR_INVALID, f"{who}: the workspace must be contiguous on the current device")
-    return _ptr(t), t.numel() * t.element_size()
+    return t.data_ptr(), t.nbytes
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _stream_of(device, stream):
+    """As _stream, for calls whose device is known: the current stream's handle without the object around it."""
+    if stream is None:
+        import torch
+        return torch._C._cuda_getCurrentRawStream(device)
+    return getattr(stream, "cuda_stream", stream)
 
 
 @functools.lru_cache(maxsize=256)
@@ -445,8 +457,8 @@ def veda_teacher(layout, q_t, k_t, teacher, row_lse=None, stream=None):
           ("teacher", teacher, torch.float32, (n, nv, nv)))
     if row_lse is not None:
         _need("veda_teacher", dev, ("row_lse", row_lse, torch.float32, (n, layout.seq_len)))
-    _check(lib().veda_teacher(layout.handle, _ptr(q_t), _ptr(k_t), n, shape[2], _ptr(row_lse), _ptr(teacher),
-                              _stream(stream)))
+    _check(lib().veda_teacher(layout.handle, _addr(q_t), _addr(k_t), n, shape[2], _addr(row_lse), _addr(teacher),
+                              _stream_of(dev, stream)))
 
 
 def veda_bias_buckets(reach, far):
@@ -483,9 +495,9 @@ def veda_score_bias(layout, feats_q, feats_k, proj_q, proj_k, reach, far, bias, 
     if bias is not None:
         spec, buckets = _bias_spec(tuple(reach), tuple(far))
         _need("veda_score_bias", dev, ("bias", bias, f32, (n, buckets)))
-    _check(lib().veda_score_bias(layout.handle, _ptr(feats_q), _ptr(feats_k), n, dim, _ptr(proj_q), _ptr(proj_k),
-                                 None if spec is None else C.byref(spec), _ptr(bias), _ptr(hats),
-                                 *_workspace("veda_score_bias", dev, workspace), _ptr(scores), _stream(stream)))
+    _check(lib().veda_score_bias(layout.handle, _addr(feats_q), _addr(feats_k), n, dim, _addr(proj_q), _addr(proj_k),
+                                 None if spec is None else C.byref(spec), _addr(bias), _addr(hats),
+                                 *_workspace("veda_score_bias", dev, workspace), _addr(scores), _stream_of(dev, stream)))
 
 
 def veda_bias_backward_workspace_bytes(layout, n_heads, reach):
@@ -499,8 +511,8 @@ def veda_bias_backward(layout, d_scores, reach, far, workspace, d_bias, stream=N
     spec, buckets = _bias_spec(tuple(reach), tuple(far))
     _need("veda_bias_backward", dev, ("d_scores", d_scores, torch.float32, (n, nv, nv)),
           ("d_bias", d_bias, torch.float32, (n, buckets)))
-    _check(lib().veda_bias_backward(layout.handle, _ptr(d_scores), n, C.byref(spec),
-                                    *_workspace("veda_bias_backward", dev, workspace), _ptr(d_bias), _stream(stream)))
+    _check(lib().veda_bias_backward(layout.handle, _addr(d_scores), n, C.byref(spec),
+                                    *_workspace("veda_bias_backward", dev, workspace), _addr(d_bias), _stream_of(dev, stream)))
 
 
 def veda_distill(layout, scores, t_idx, t_val, t_cnt, tau, loss, d_scores=None, row_weight=None, by_column=False,
@@ -518,9 +530,9 @@ def veda_distill(layout, scores, t_idx, t_val, t_cnt, tau, loss, d_scores=None, 
         _need("veda_distill", dev, ("d_scores", d_scores, f32, (n, nv, nv)))
     if row_weight is not None:
         _need("veda_distill", dev, ("row_weight", row_weight, f32, (n, nv)))
-    _check(lib().veda_distill(layout.handle, _ptr(scores), n, _ptr(t_idx), _ptr(t_val), _ptr(t_cnt), width,
-                              int(by_column), float(tau), _ptr(row_weight), _ptr(loss), _ptr(d_scores),
-                              _stream(stream)))
+    _check(lib().veda_distill(layout.handle, _addr(scores), n, _addr(t_idx), _addr(t_val), _addr(t_cnt), width,
+                              int(by_column), float(tau), _addr(row_weight), _addr(loss), _addr(d_scores),
+                              _stream_of(dev, stream)))
 
 
 def veda_score_backward_workspace_bytes(layout, n_heads, dim):
@@ -540,8 +552,8 @@ def veda_score_backward(layout, feats_q, feats_k, hats, d_scores, workspace, d_p
           ("d_scores", d_scores, f32, (n, nv, nv)), ("d_proj_q", d_proj_q, f32, (n, 3 * dim, dim)),
           ("d_proj_k", d_proj_k, f32, (n, 3 * dim, dim)))
     ws, size = _workspace("veda_score_backward", dev, workspace)
-    _check(lib().veda_score_backward(layout.handle, _ptr(feats_q), _ptr(feats_k), n, dim, _ptr(hats), _ptr(d_scores),
-                                     _ptr(d_proj_q), _ptr(d_proj_k), ws, size, _stream(stream)))
+    _check(lib().veda_score_backward(layout.handle, _addr(feats_q), _addr(feats_k), n, dim, _addr(hats), _addr(d_scores),
+                                     _addr(d_proj_q), _addr(d_proj_k), ws, size, _stream_of(dev, stream)))
 
 
 def veda_sync_status(stream=None):

@@ -47,25 +47,34 @@ __host__ __device__ __forceinline__ int bias_bucket(const BiasClasses& b, int dt
 // index as a key (its number) and as a query (where the table's part of its span is centred, less its number). Tiles are
 // in (h, w, t) order, t fastest, and so are the numbers: neighbouring keys read neighbouring entries.
 
-// table[head][o] = factor bias[head][bucket(o)]: the sums that start from it are scaled by 1 / factor at their end
-__global__ void __launch_bounds__(256) bias_expand_kernel(const float* bias, float* table, float factor, BiasClasses b,
-                                                          const int4* span_grid, int n_spans, int count) {
-    const int i = blockIdx.x * 256 + threadIdx.x;
-    if (i >= count + 2) return;
-    int bucket = b.buckets - 2 + (i - count);
-    if (i < count) {
+// The table, written by otherwise idle warps of the launch that computes the projected features (train_gemm.cuh):
+// table[head][o] = factor bias[head][bucket(o)]; the sums that start from it are scaled by 1 / factor at their end.
+struct BiasExpand {
+    const float* bias;  // [heads, buckets], or null: no table
+    float* table;       // [heads, count + 2]
+    float factor;
+    const int4* span_grid;
+    int n_spans, count, heads;
+    BiasClasses b;
+};
+
+// entry i of every head's table
+__device__ __forceinline__ void bias_expand(const BiasExpand& x, int i) {
+    int bucket = x.b.buckets - 2 + (i - x.count);
+    if (i < x.count) {
         int o = i;
-        int4 g = span_grid[0];
-        for (int s = 0; s < n_spans; ++s) {
-            g = span_grid[s];
+        int4 g = x.span_grid[0];
+        for (int s = 0; s < x.n_spans; ++s) {
+            g = x.span_grid[s];
             const int offsets = (2 * g.y - 1) * (2 * g.z - 1) * (2 * g.w - 1);
             if (o < offsets) break;
             o -= offsets;
         }
         const int rt = 2 * g.y - 1, rw = 2 * g.w - 1;
-        bucket = bias_bucket(b, o % rt - (g.y - 1), o / (rt * rw) - (g.z - 1), (o / rt) % rw - (g.w - 1));
+        bucket = bias_bucket(x.b, o % rt - (g.y - 1), o / (rt * rw) - (g.z - 1), (o / rt) % rw - (g.w - 1));
     }
-    table[int64_t(blockIdx.y) * (count + 2) + i] = factor * bias[int64_t(blockIdx.y) * b.buckets + bucket];
+    for (int h = 0; h < x.heads; ++h)
+        x.table[int64_t(h) * (x.count + 2) + i] = x.factor * x.bias[int64_t(h) * x.b.buckets + bucket];
 }
 
 struct BiasBackwardArgs {
@@ -110,6 +119,7 @@ __device__ __forceinline__ void bias_interval(const int* starts, int reach, int 
 template <int kPer, bool kOneSpan>
 __global__ void __launch_bounds__(512, kPer <= 4 ? 2 : 1) bias_backward_kernel(const BiasBackwardArgs a) {
     constexpr int kDepth = kPer <= 2 ? 8 : kPer <= 4 ? 4 : 2;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     extern __shared__ float sums[];  // [offsets], then 2 x 16 for the cross-span sums of the warps
     const int head = blockIdx.y, pairs = a.b.buckets - 2, nt = blockDim.x;
     const int i0 = blockIdx.x * a.rows_per_chunk, i1 = min(a.n, i0 + a.rows_per_chunk);
@@ -236,13 +246,20 @@ __global__ void __launch_bounds__(256) bias_backward_wide_kernel(const BiasBackw
     }
 }
 
-// d_bias[head][b] = the chunks' sums, added in chunk order
-__global__ void __launch_bounds__(256) bias_reduce_kernel(const float* partial, float* d_bias, int chunks, int buckets) {
-    const int b = blockIdx.x * 256 + threadIdx.x;
+// d_bias[head][b] = the chunks' sums, added in chunk order, eight loads at a time (a programmatic dependent launch)
+__global__ void __launch_bounds__(128) bias_reduce_kernel(const float* partial, float* d_bias, int chunks, int buckets) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int b = blockIdx.x * 128 + threadIdx.x;
     if (b >= buckets) return;
     const float* p = partial + int64_t(blockIdx.y) * chunks * buckets + b;
     float sum = 0.f;
-    for (int c = 0; c < chunks; ++c) sum += p[int64_t(c) * buckets];
+    for (int c = 0; c < chunks; c += 8) {
+        float v[8];
+#pragma unroll
+        for (int x = 0; x < 8; ++x) v[x] = c + x < chunks ? p[int64_t(c + x) * buckets] : 0.f;
+#pragma unroll
+        for (int x = 0; x < 8; ++x) sum += v[x];
+    }
     d_bias[int64_t(blockIdx.y) * buckets + b] = sum;
 }
 

@@ -11,7 +11,9 @@
 // between them: up to 32 columns a thread, one warp for a row of up to 1024 columns and 2 to 16 warps beyond. Its
 // exponentials are taken once (2^x of (s - max) log2(e) / tau), serve both the sum and the gradient, and only the
 // listed columns, a tenth of the row or less, are visited again: they are written as q, and after a barrier as q - p.
-// Lists are read three times (largest logit, sums, gradient) and come from L1 after the first.
+// What bounds it beside the bytes is the chain of latencies of a row (count, list, listed scores, two rounds of
+// reductions), so the count, the first kListed entries of the list and the row are loaded together, entries behind the
+// count among them, which nothing uses; longer lists read the rest again where they need it.
 #pragma once
 
 #include <cuda_runtime.h>
@@ -24,6 +26,7 @@
 namespace veda {
 
 constexpr int kErrDistillList = 2;  // the latched bit of a malformed list, as the attend's
+constexpr int kListed = 4;          // list entries a thread keeps in registers
 
 struct DistillArgs {
     const float* scores;      // [n_heads * n, n]
@@ -69,29 +72,37 @@ __global__ void __launch_bounds__(kWarps == 1 ? 128 : 32 * kWarps) distill_kerne
     const auto maxf = [](float x, float y) { return fmaxf(x, y); };
     const auto add = [](float x, float y) { return x + y; };
 
+    const int given = a.t_cnt[r];
     float v[kPer];
 #pragma unroll
     for (int k = 0; k < kPer; ++k) {
         const int j = lane + kLanes * k;
         v[k] = j < a.n ? __ldg(s + j) : -INFINITY;
     }
+    int id[kListed], before[kListed];
+    float t[kListed], x[kListed];
+#pragma unroll
+    for (int u = 0; u < kListed; ++u) {
+        const int e = lane + kLanes * u;
+        id[u] = e < a.width ? __ldg(idx + e) : -1;
+        before[u] = e < a.width && e > 0 ? __ldg(idx + e - 1) : -1;
+        t[u] = e < a.width && !a.by_column ? __ldg(val + e) : 0.f;
+    }
     // the list: its entries are ascending tile ids; it is cut at the first bad one, and ids from n on (global tiles,
     // which no score column stands for) end the part that counts
-    const int given = a.t_cnt[r];
     bool bad = given < 0 || given > a.width;
     int cnt = max(0, min(given, a.width));
-    float mt = -INFINITY;
     {
         int end = cnt;
-        for (int e = lane; e < cnt; e += kLanes) {
-            const int id = idx[e];
-            const bool wrong = id < 0 || id >= a.n_tiles || (e > 0 && id <= idx[e - 1]);
+        const auto check = [&](int e, int mine, int previous) {
+            const bool wrong = mine < 0 || mine >= a.n_tiles || mine <= previous;
             bad |= wrong;
-            if (wrong || id >= a.n) {
-                end = e;
-                break;
-            }
-        }
+            if (wrong || mine >= a.n) end = min(end, e);
+        };
+#pragma unroll
+        for (int u = 0; u < kListed; ++u)
+            if (lane + kLanes * u < end) check(lane + kLanes * u, id[u], before[u]);
+        for (int e = lane + kLanes * kListed; e < end; e += kLanes) check(e, idx[e], idx[e - 1]);
         if constexpr (kWarps == 1) {
             cnt = __reduce_min_sync(0xffffffffu, end);
         } else {
@@ -103,7 +114,16 @@ __global__ void __launch_bounds__(kWarps == 1 ? 128 : 32 * kWarps) distill_kerne
         }
         if (bad) atomicOr(a.err, kErrDistillList);
     }
-    for (int e = lane; e < cnt; e += kLanes) mt = fmaxf(mt, val[a.by_column ? idx[e] : e]);
+    float mt = -INFINITY;
+#pragma unroll
+    for (int u = 0; u < kListed; ++u) {
+        const bool on = lane + kLanes * u < cnt;
+        x[u] = on ? __ldg(s + id[u]) : 0.f;
+        if (a.by_column && on) t[u] = __ldg(val + id[u]);
+        if (!on) t[u] = -INFINITY;
+        mt = fmaxf(mt, t[u]);
+    }
+    for (int e = lane + kLanes * kListed; e < cnt; e += kLanes) mt = fmaxf(mt, val[a.by_column ? idx[e] : e]);
     float ms = -INFINITY;
 #pragma unroll
     for (int k = 0; k < kPer; ++k) ms = fmaxf(ms, v[k]);
@@ -119,14 +139,17 @@ __global__ void __launch_bounds__(kWarps == 1 ? 128 : 32 * kWarps) distill_kerne
         zs += v[k];
     }
     float zt = 0.f, gap = 0.f;
-    for (int e = lane; e < cnt; e += kLanes) {
-        const int id = idx[e];
-        const float t = val[a.by_column ? id : e];
-        if (t == -INFINITY) continue;
-        const float p = ptx::ex2((t - mt) * c2);
+    // a listed logit becomes its exponential; -inf has no mass
+    const auto entry = [&](float logit, float score) {
+        if (logit == -INFINITY) return 0.f;
+        const float p = ptx::ex2((logit - mt) * c2);
         zt += p;
-        if (!(p == 0.f)) gap += p * (((t - mt) - (__ldg(s + id) - ms)) * a.inv_tau);
-    }
+        if (!(p == 0.f)) gap += p * (((logit - mt) - (score - ms)) * a.inv_tau);
+        return p;
+    };
+#pragma unroll
+    for (int u = 0; u < kListed; ++u) t[u] = entry(t[u], x[u]);
+    for (int e = lane + kLanes * kListed; e < cnt; e += kLanes) entry(val[a.by_column ? idx[e] : e], __ldg(s + idx[e]));
     zs = row_reduce<kWarps>(zs, scratch[0], add);
     zt = row_reduce<kWarps>(zt, scratch[1], add);
     if constexpr (kWarps > 1) __syncthreads();
@@ -147,11 +170,13 @@ __global__ void __launch_bounds__(kWarps == 1 ? 128 : 32 * kWarps) distill_kerne
     if constexpr (kWarps == 1) __syncwarp();
     else __syncthreads();
     const float izt = 1.f / zt;
-    for (int e = lane; e < cnt; e += kLanes) {
-        const int id = idx[e];
-        const float t = val[a.by_column ? id : e], x = __ldg(s + id);
-        const float q = x == -INFINITY ? 0.f : ptx::ex2((x - ms) * c2) * iz;
-        d[id] = c * (q - (t == -INFINITY ? 0.f : ptx::ex2((t - mt) * c2) * izt));
+    const auto mass = [&](float score) { return score == -INFINITY ? 0.f : ptx::ex2((score - ms) * c2) * iz; };
+#pragma unroll
+    for (int u = 0; u < kListed; ++u)
+        if (lane + kLanes * u < cnt) d[id[u]] = c * (mass(x[u]) - t[u] * izt);
+    for (int e = lane + kLanes * kListed; e < cnt; e += kLanes) {
+        const float logit = val[a.by_column ? idx[e] : e];
+        d[idx[e]] = c * (mass(__ldg(s + idx[e])) - (logit == -INFINITY ? 0.f : ptx::ex2((logit - mt) * c2) * izt));
     }
 }
 

@@ -19,6 +19,7 @@
 //   warp 0       MMA issuer, 12 MMAs per slice; warp 1 owns the TMEM: the sums twice (columns 0-255) and kStages
 //                stages of A's hi and lo parts (256-511)
 //   warp 2       TMA producer: raw slices of both operands into the split groups' stages
+//   warps 1, 3   the bias table that the score launch after this one reads, where it is asked for
 //   warps 4-11   epilogue, two warps per lane quarter with half of the columns each; their sums start from what is added
 //                to the product, whose loads pass while the tile is computed
 //   warps 12-23  split, three groups with a stage each that take the slices in turn, so that one group's waits pass while
@@ -39,6 +40,7 @@
 
 #include <cstdint>
 
+#include "bias.cuh"
 #include "ptx.cuh"
 #include "tf32.cuh"
 #include "wait.cuh"
@@ -271,7 +273,8 @@ __device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_
         : "memory");
 }
 
-__global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Args a) {
+__global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Args a,
+                                                           const __grid_constant__ BiasExpand expand) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     Bars& B = *reinterpret_cast<Bars*>(smem + kOffBar);
@@ -302,6 +305,9 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
     __syncthreads();
     ptx::tc_fence_after();
     const uint32_t tmem = *tmem_slot;
+    // (programmatic dependent launch: what is above may run while the launch before this one still does)
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
 
     if (warp < 4) {
         ptx::regs_dec<56>();
@@ -378,6 +384,9 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
                 for (int k = (g > kStages ? g - kStages : 0); k < g; ++k)
                     ptx::mbar_wait(&B.raw_full[k % kStages], (k / kStages) & 1, &never, kDrainNs);
             }
+        } else if (expand.bias) {
+            // ------------------------------------------------------------------------ the bias table (warps 1 and 3)
+            for (int i = (blockIdx.x * 2 + (warp >> 1)) * 32 + lane; i < expand.count + 2; i += gridDim.x * 64) bias_expand(expand, i);
         }
     } else if (warp < 12) {
         // ---------------------------------------------------------------------------- epilogue

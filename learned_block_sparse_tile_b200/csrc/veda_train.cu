@@ -117,7 +117,8 @@ int operand_map(CUtensorMap* m, const train::Operand& o, int K, int batches) {
     return o.layout == train::kCols ? make_f32_cols_map(m, o.base, o.rows, K, batches) : make_f32_map(m, o.base, K, o.rows, batches);
 }
 
-int launch_gemm(const char* what, train::Args a, const DeviceInfo& di, cudaStream_t s) {
+// `after`: the launch before it on the stream is one of this call's, and its start may overlap that one's end
+int launch_gemm(const char* what, train::Args a, const BiasExpand& expand, bool after, const DeviceInfo& di, cudaStream_t s) {
     static std::atomic<bool> set[kMaxDevices];
     if (!set[di.ordinal].load()) {
         cudaError_t e = cudaFuncSetAttribute(train::gemm_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(train::kSmem));
@@ -137,7 +138,18 @@ int launch_gemm(const char* what, train::Args a, const DeviceInfo& di, cudaStrea
         if (int rc = operand_map(&m.a[i], a.set[i].a, a.K, a.nb)) return rc;
         if (int rc = operand_map(&m.b[i], a.set[i].b, a.K, a.nb)) return rc;
     }
-    train::gemm_kernel<<<unsigned(std::min(a.n_tiles, di.sms)), train::kThreads, train::kSmem, s>>>(m, a);
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(unsigned(std::min(a.n_tiles, di.sms)));
+    cfg.blockDim = dim3(train::kThreads);
+    cfg.dynamicSmemBytes = train::kSmem;
+    cfg.stream = s;
+    cudaLaunchAttribute overlap{};
+    overlap.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    overlap.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &overlap;
+    cfg.numAttrs = after ? 1 : 0;
+    cudaError_t e = cudaLaunchKernelEx(&cfg, train::gemm_kernel, m, a, expand);
+    if (e != cudaSuccess) return fail(VEDA_ERR_CUDA, std::string(what) + ": " + cudaGetErrorString(e));
     return launch_status(what);
 }
 
@@ -285,11 +297,10 @@ extern "C" int veda_score_bias(const veda_layout* layout, const float* feats_q, 
         const int offsets = layout->bias_offsets;
         cudaStream_t s = static_cast<cudaStream_t>(stream);
         float* table = static_cast<float*>(workspace);
-        if (bias) {
-            bias_expand_kernel<<<dim3((offsets + 2 + 255) / 256, n_heads), 256, 0, s>>>(
-                bias, table, float(std::sqrt(double(dim))), b, reinterpret_cast<const int4*>(dc->span_grid), int(layout->span_grid.size() / 4), offsets);
-            if (int rc = launch_status("bias_expand_kernel")) return rc;
-        }
+        BiasExpand expand{};
+        if (bias)
+            expand = {bias, table, float(std::sqrt(double(dim))), reinterpret_cast<const int4*>(dc->span_grid),
+                      int(layout->span_grid.size() / 4), offsets, n_heads, b};
         const int64_t nf = int64_t(n) * 3 * dim, nd = int64_t(n) * dim;
         // hats[tile][d], both sides in one launch, then scores[query][key]
         train::Args p{};
@@ -306,7 +317,7 @@ extern "C" int veda_score_bias(const veda_layout* layout, const float* feats_q, 
             p.set[side] = {operand(side ? proj_k : proj_q, dim, 3 * dim, true), operand(f, n, 3 * dim, false),
                            hats + side * n_heads * nd, f};
         }
-        if (int rc = launch_gemm("veda_score_bias (projections)", p, di, s)) return rc;
+        if (int rc = launch_gemm("veda_score_bias (projections)", p, expand, false, di, s)) return rc;
         train::Args l{};
         l.n_sets = 1;
         l.nb = n_heads;
@@ -319,7 +330,7 @@ extern "C" int veda_score_bias(const veda_layout* layout, const float* feats_q, 
         l.tile_num = reinterpret_cast<const int4*>(dc->tile_num);
         l.table_stride = offsets + 2;
         l.offsets = offsets;
-        return launch_gemm("veda_score_bias (logits)", l, di, s);
+        return launch_gemm("veda_score_bias (logits)", l, BiasExpand{}, true, di, s);
     });
 }
 
@@ -375,7 +386,17 @@ extern "C" int veda_bias_backward(const veda_layout* layout, const float* d_scor
                                : launch_bias<16>(one, a, chunks, n_heads, di, s);
         }
         if (rc) return rc;
-        bias_reduce_kernel<<<dim3((a.b.buckets + 255) / 256, n_heads), 256, 0, s>>>(a.partial, d_bias, chunks, a.b.buckets);
+        cudaLaunchConfig_t cfg{};
+        cfg.gridDim = dim3(unsigned(a.b.buckets + 127) / 128, unsigned(n_heads));
+        cfg.blockDim = dim3(128);
+        cfg.stream = s;
+        cudaLaunchAttribute overlap{};
+        overlap.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        overlap.val.programmaticStreamSerializationAllowed = 1;
+        cfg.attrs = &overlap;
+        cfg.numAttrs = 1;
+        cudaError_t e = cudaLaunchKernelEx(&cfg, bias_reduce_kernel, static_cast<const float*>(a.partial), d_bias, chunks, int(a.b.buckets));
+        if (e != cudaSuccess) return fail(VEDA_ERR_CUDA, std::string("bias_reduce_kernel: ") + cudaGetErrorString(e));
         return launch_status("bias_reduce_kernel");
     });
 }
@@ -475,7 +496,7 @@ extern "C" int veda_score_backward(const veda_layout* layout, const float* feats
             p.set[side] = {operand(dx + side * n_heads * nd, dim, n, true), operand(side ? feats_k : feats_q, 3 * dim, n, true),
                            side ? d_proj_k : d_proj_q, nullptr};
         }
-        if (int rc = launch_gemm("veda_score_backward (projected features)", x, di, s)) return rc;
-        return launch_gemm("veda_score_backward (projections)", p, di, s);
+        if (int rc = launch_gemm("veda_score_backward (projected features)", x, BiasExpand{}, false, di, s)) return rc;
+        return launch_gemm("veda_score_backward (projections)", p, BiasExpand{}, true, di, s);
     });
 }
