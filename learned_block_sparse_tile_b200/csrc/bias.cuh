@@ -112,20 +112,23 @@ __device__ __forceinline__ void bias_interval(const int* starts, int reach, int 
 
 // Sums of one chunk of query rows, by offset first. Within a row no two keys of the query's span have the same offset, so
 // a row adds to as many different sums as it has columns: the CTA keeps one sum per offset in shared memory (fewer than 8
-// per tile), its threads add a row's columns without collisions, and a barrier parts the rows. Nothing is atomic, and
-// every sum is added up in row order. The loads run kDepth rows ahead in registers, because the rows' own work is short:
-// an addition in shared memory and a barrier. At the end each bucket is the sum of a box of offsets.
-// Bound by the barriers, about 100 cycles a row, with two CTAs on an SM taking turns; reading d_scores is the floor.
+// per tile), its threads add a row's columns without collisions, and a barrier parts the rows. Up to 1024 tiles there are
+// two sets of sums, for even and odd rows, and a barrier parts pairs of rows (104k rows, 24 heads: 26 -> 25 us). Nothing
+// is atomic, and every sum is added up in row order. The loads run kDepth rows ahead in registers, because the rows' own
+// work is short: an addition in shared memory and a barrier. At the end each bucket is the sum of a box of offsets.
+// Bound by the chain of shared-memory addition and barrier, with two CTAs on an SM taking turns; the floor is reading
+// d_scores once.
 template <int kPer, bool kOneSpan>
 __global__ void __launch_bounds__(512, kPer <= 4 ? 2 : 1) bias_backward_kernel(const BiasBackwardArgs a) {
     constexpr int kDepth = kPer <= 2 ? 8 : kPer <= 4 ? 4 : 2;
+    constexpr int kSets = kPer <= 2 ? 2 : 1;  // row i adds to set i % kSets
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    extern __shared__ float sums[];  // [offsets], then 2 x 16 for the cross-span sums of the warps
+    extern __shared__ float sums[];  // [kSets][offsets], 2 x 16 cross-span sums of the warps, then the rows' queries
     const int head = blockIdx.y, pairs = a.b.buckets - 2, nt = blockDim.x;
     const int i0 = blockIdx.x * a.rows_per_chunk, i1 = min(a.n, i0 + a.rows_per_chunk);
-    const float* src = a.d_scores + int64_t(head) * a.n * a.n;
+    int2* query = reinterpret_cast<int2*>(sums + (kSets * a.offsets + 32 + 1) / 2 * 2);  // {span, number}
+    const float* next = a.d_scores + (int64_t(head) * a.n + i0) * a.n + threadIdx.x;     // of the next row to load
     float v[kDepth][kPer];
-    int2 query[kDepth];  // {span, number} of the rows in flight
     int span[kPer], num[kPer];
 #pragma unroll
     for (int k = 0; k < kPer; ++k) {
@@ -134,38 +137,42 @@ __global__ void __launch_bounds__(512, kPer <= 4 ? 2 : 1) bias_backward_kernel(c
         span[k] = j < a.n ? key.x : -1;
         num[k] = key.y;
     }
-    const auto load = [&](float (&x)[kPer], int2& q, int i) {
-        if (i >= i1) return;
-        const int4 t = a.tile_num[i];
-        q = make_int2(t.x, t.z);
-        const float* p = src + int64_t(i) * a.n + threadIdx.x;
+    const auto load = [&](float (&x)[kPer]) {
 #pragma unroll
-        for (int k = 0; k < kPer; ++k) x[k] = threadIdx.x + nt * k < a.n ? __ldg(p + nt * k) : 0.f;
+        for (int k = 0; k < kPer; ++k) x[k] = span[k] >= 0 ? __ldg(next + nt * k) : 0.f;
+        next += a.n;
     };
 #pragma unroll
-    for (int r = 0; r < kDepth; ++r) load(v[r], query[r], i0 + r);
-    for (int o = threadIdx.x; o < a.offsets; o += nt) sums[o] = 0.f;
+    for (int r = 0; r < kDepth; ++r)
+        if (i0 + r < i1) load(v[r]);
+    for (int i = i0 + threadIdx.x; i < i1; i += nt) {
+        const int4 q = a.tile_num[i];
+        query[i - i0] = make_int2(q.x, q.z);
+    }
+    for (int o = threadIdx.x; o < kSets * a.offsets; o += nt) sums[o] = 0.f;
     __syncthreads();
     float before = 0.f, behind = 0.f;
     for (int i = i0; i < i1; i += kDepth) {
 #pragma unroll
         for (int r = 0; r < kDepth; ++r) {
             if (i + r < i1) {
+                const int2 q = query[i - i0 + r];
+                float* at = sums + (r % kSets) * a.offsets + q.y;
 #pragma unroll
                 for (int k = 0; k < kPer; ++k) {
-                    if (kOneSpan ? span[k] >= 0 : span[k] == query[r].x) {
-                        sums[num[k] + query[r].y] += v[r][k];
+                    if (kOneSpan ? span[k] >= 0 : span[k] == q.x) {
+                        at[num[k]] += v[r][k];
                     } else if (!kOneSpan) {  // (threads past the row hold zeros)
-                        before += span[k] < query[r].x ? v[r][k] : 0.f;
-                        behind += span[k] > query[r].x ? v[r][k] : 0.f;
+                        before += span[k] < q.x ? v[r][k] : 0.f;
+                        behind += span[k] > q.x ? v[r][k] : 0.f;
                     }
                 }
-                load(v[r], query[r], i + r + kDepth);
-                __syncthreads();
+                if (i + r + kDepth < i1) load(v[r]);
             }
+            if (r % kSets == kSets - 1) __syncthreads();
         }
     }
-    float* cross = sums + a.offsets;
+    float* cross = sums + kSets * a.offsets;
 #pragma unroll
     for (int o = 16; o; o >>= 1) {
         before += __shfl_xor_sync(0xffffffffu, before, o);
@@ -193,7 +200,11 @@ __global__ void __launch_bounds__(512, kPer <= 4 ? 2 : 1) bias_backward_kernel(c
                 bias_interval(a.b.starts[2], a.b.reach[2], b % iw, g.w - 1, rw, w0, w1);
                 for (int h = h0; h < h1; ++h)
                     for (int w = w0; w < w1; ++w)
-                        for (int t = t0; t < t1; ++t) sum += at[(h * rw + w) * rt + t];
+#pragma unroll 4
+                        for (int t = t0; t < t1; ++t) {
+                            const float* x = at + (h * rw + w) * rt + t;
+                            sum += kSets == 2 ? x[0] + x[a.offsets] : x[0];
+                        }
                 at += rt * rh * rw;
             }
         }

@@ -172,6 +172,8 @@ int bias_chunks(int n, int n_heads) {
 }
 
 constexpr int kBiasMaxSmem = 227 * 1024;
+// one or two sets of sums, the warps' cross-span sums, and a query of 8 bytes per row
+size_t bias_smem(int per, int offsets, int rows) { return ((per <= 2 ? 2 : 1) * size_t(offsets) + 32 + 1) / 2 * 8 + size_t(rows) * 8; }
 
 template <int kPer, bool kOneSpan>
 int launch_bias_backward(const BiasBackwardArgs& a, int chunks, int n_heads, const DeviceInfo& di, cudaStream_t s) {
@@ -183,7 +185,7 @@ int launch_bias_backward(const BiasBackwardArgs& a, int chunks, int n_heads, con
         set[di.ordinal].store(true);
     }
     const int threads = std::max(128, ((a.n + kPer - 1) / kPer + 31) / 32 * 32);
-    bias_backward_kernel<kPer, kOneSpan><<<dim3(chunks, n_heads), threads, (a.offsets + 32) * sizeof(float), s>>>(a);
+    bias_backward_kernel<kPer, kOneSpan><<<dim3(chunks, n_heads), threads, bias_smem(kPer, a.offsets, a.rows_per_chunk), s>>>(a);
     return launch_status("bias_backward_kernel");
 }
 
@@ -370,7 +372,7 @@ extern "C" int veda_bias_backward(const veda_layout* layout, const float* d_scor
         const int chunks = bias_chunks(a.n, n_heads);
         cudaStream_t s = static_cast<cudaStream_t>(stream);
         int rc;
-        if ((a.offsets + 32) * int(sizeof(float)) > kBiasMaxSmem || a.n > 8192) {
+        if (bias_smem(a.n <= 1024 ? 2 : 4, a.offsets, a.rows_per_chunk) > size_t(kBiasMaxSmem) || a.n > 8192) {
             const int smem = a.n * int(sizeof(float));
             cudaError_t e = cudaFuncSetAttribute(bias_backward_wide_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
             if (e != cudaSuccess)
