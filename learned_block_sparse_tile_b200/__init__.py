@@ -3,7 +3,7 @@
 ``from learned_block_sparse_tile_b200 import veda_plan, veda_gather, veda_score, veda_select, veda_attend``
 gives the raw entry points (same names as ``include/veda.h``); ``VedaLayer`` runs a whole layer and
 ``HostPipeline`` runs consecutive independent layer calls on pinned host tensors with the PCIe transfers
-overlapped with the kernels.
+overlapped with the kernels. ``PredictorTrainer`` trains a layer's tile predictor: teacher, loss and gradients.
 """
 from ._lib import (  # noqa: F401
     EXPORTS, LIB_PATH, TILE, VEDA_ERR_BAD_LIST, VEDA_ERR_CUDA, VEDA_ERR_INVALID, VEDA_ERR_TIMEOUT,
@@ -18,3 +18,4 @@ from ._lib import (  # noqa: F401
 )
 from .layer import VedaLayer  # noqa: F401
 from .pipeline import HostPipeline  # noqa: F401
+from .train import PredictorTrainer  # noqa: F401

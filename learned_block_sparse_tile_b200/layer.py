@@ -104,6 +104,7 @@ class VedaLayer:
             self.groups.append(g)
         self.launches = ((self.LAUNCHES_PER_GROUP_DIRECT if self.direct else self.LAUNCHES_PER_GROUP) +
                          (self.EXTRA_LAUNCHES_PAIRED if self.paired else 0)) * len(self.groups)
+        self.bias_spec = None  # (reach, far) of set_bias
         self._side = torch.cuda.Stream(self.device)  # the V gathers
 
     def set_projections(self, proj_q, proj_k):
@@ -112,6 +113,38 @@ class VedaLayer:
             idx = torch.tensor(g["heads_list"], dtype=torch.long)
             g["proj_q"] = proj_q.index_select(0, idx).to(self.device, torch.float32).contiguous()
             g["proj_k"] = proj_k.index_select(0, idx).to(self.device, torch.float32).contiguous()
+
+    def set_bias(self, reach=None, far=None, bias=None):
+        """A learned relative position bias of the tile scores (veda_score_bias): per-axis (t, h, w) reaches and far
+        distances in tiles, and bias fp32 [H, buckets] (any device; veda_bias_buckets gives the number). Selection then
+        ranks score + bias. No arguments: no bias, the scores of veda_score."""
+        if bias is None and (reach is not None or far is not None):
+            raise ValueError("VedaLayer.set_bias: reach and far come with a bias")
+        buckets = None if bias is None else L.veda_bias_buckets(reach, far)
+        if bias is not None and tuple(bias.shape) != (self.heads, buckets):
+            raise ValueError(f"VedaLayer.set_bias: bias must be [{self.heads}, {buckets}], not {tuple(bias.shape)}")
+        had = self.bias_spec is not None
+        self.bias_spec = None if bias is None else (tuple(reach), tuple(far))
+        self.launches += ((bias is None) - (not had)) * len(self.groups)  # one launch fewer per group with a bias
+        for g in self.groups:
+            for key in ("bias", "hats", "bias_ws"):
+                g.pop(key, None)
+            if bias is None:
+                continue
+            n, lay = len(g["heads_list"]), g["layout"]
+            idx = torch.tensor(g["heads_list"], dtype=torch.long, device=bias.device)
+            g["bias"] = bias.index_select(0, idx).to(self.device, torch.float32).contiguous()
+            g["hats"] = torch.empty(2, n, lay.n_video, self.dim, dtype=torch.float32, device=self.device)
+            g["bias_ws"] = torch.empty(L.veda_score_bias_workspace_bytes(lay, n, self.dim), dtype=torch.uint8,
+                                       device=self.device)
+
+    def _score(self, g, stream):
+        lay = g["layout"]
+        if self.bias_spec is None:
+            L.veda_score(lay, g["feats_q"], g["feats_k"], g["proj_q"], g["proj_k"], g["workspace"], g["scores"], stream)
+        else:
+            L.veda_score_bias(lay, g["feats_q"], g["feats_k"], g["proj_q"], g["proj_k"], *self.bias_spec, g["bias"],
+                              g["hats"], g["bias_ws"], g["scores"], stream)
 
     def kept_tiles(self):
         """Total kept (video query tile, key tile) pairs of the last forward, per the page's ``kept``."""
@@ -170,8 +203,7 @@ class VedaLayer:
                 L.veda_pool(lay, k, g["heads"], g["feats_k"], st, max_sq=g["k_max_sq"])
                 done(m, st)
                 m = mark("score", st)
-                L.veda_score(lay, g["feats_q"], g["feats_k"], g["proj_q"], g["proj_k"], g["workspace"], g["scores"],
-                             st)
+                self._score(g, st)
                 done(m, st)
                 m = mark("select", st)
                 L.veda_select(lay, g["scores"], g["kept_idx"], g["kept_cnt"], st)
@@ -203,7 +235,7 @@ class VedaLayer:
             v_done = torch.cuda.Event()
             v_done.record(side)
             m = mark("score", st)
-            L.veda_score(lay, g["feats_q"], g["feats_k"], g["proj_q"], g["proj_k"], g["workspace"], g["scores"], st)
+            self._score(g, st)
             done(m, st)
             m = mark("select", st)
             L.veda_select(lay, g["scores"], g["kept_idx"], g["kept_cnt"], st)
