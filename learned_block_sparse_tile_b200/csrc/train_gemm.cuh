@@ -135,38 +135,51 @@ __device__ __forceinline__ float load1(const float* p) {
     return v;
 }
 
+// a box of a tensor map into L2
+__device__ __forceinline__ void prefetch_3d(const void* desc, int32_t c0, int32_t c1, int32_t c2) {
+    asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global [%0, {%1, %2, %3}];" ::"l"(reinterpret_cast<uint64_t>(desc)), "r"(c0),
+                 "r"(c1), "r"(c2)
+                 : "memory");
+}
+
 // sixteen bytes global -> shared in the background
 __device__ __forceinline__ void copy16(uint32_t dst, const float* src) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 
-// A warp's pieces of a slice of an operand without a tensor map, as element numbers in the whole tensor (of `total`): its 32
-// rows (kRows), or its 32 columns of every k (kCols).
+// A warp's pieces of a slice of an operand without a tensor map: its 32 rows (kRows), or its 32 columns of every k (kCols).
 struct Pieces {
-    int64_t first;   // element of (the warp's first row, k0)
-    int64_t total;
-    int64_t step;    // between pieces: a row, or a k
+    const float* first;   // element (the warp's first row, k0)
+    const float* whole;   // the tensor's end, less what fills no 16 bytes
+    const float* end;
+    uint32_t step;        // elements between pieces: a row, or a k
     __device__ __forceinline__ Pieces(const Operand& o, int batch, int r0, int k0, int nb) {
-        first = batch * o.batch + (o.layout == kCols ? int64_t(k0) * o.stride + r0 : int64_t(r0) * o.stride + k0);
-        total = nb * o.batch;
-        step = o.stride;
+        first = o.base + batch * o.batch + (o.layout == kCols ? int64_t(k0) * o.stride + r0 : int64_t(r0) * o.stride + k0);
+        end = o.base + nb * o.batch;
+        whole = o.base + ((nb * o.batch) & ~int64_t(3));
+        step = uint32_t(o.stride);
     }
+    __device__ __forceinline__ const float* piece(int x) const { return first + uint32_t(x) * step; }
+    // the 16-byte boundary before p, and p's place behind it (the tensor's base is 16-byte aligned)
+    static __device__ __forceinline__ const float* boundary(const float* p) {
+        return reinterpret_cast<const float*>(reinterpret_cast<uintptr_t>(p) & ~uintptr_t(15));
+    }
+    static __device__ __forceinline__ uint32_t place(const float* p) { return (uint32_t(reinterpret_cast<uintptr_t>(p)) >> 2) & 3; }
     // The warp copies 32 pieces of nine 16-byte parts: eight parts of four pieces at a time, then the ninth of all (needed
     // only where a piece starts past its boundary). Parts that are not whole inside the tensor are left out; pieces past
     // the operand's rows or K hold other values of the tensor, which nothing uses.
-    __device__ __forceinline__ void copy(uint32_t dst, const float* base, int lane) const {
-        const int64_t whole = total & ~int64_t(3);
-        int64_t e = first + (lane >> 3) * step;
-        dst += 4 * ((lane >> 3) * kPitch + 4 * (lane & 7));
+    __device__ __forceinline__ void copy(uint32_t dst, int lane) const {
+        const uint32_t to = dst + 4 * ((lane >> 3) * kPitch + 4 * (lane & 7));
+        const float* p = piece(lane >> 3);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            const int64_t at = (e & ~int64_t(3)) + 4 * (lane & 7);
-            if (at < whole) copy16(dst + 16 * j * kPitch, base + at);
-            e += 4 * step;
+            const float* at = boundary(p) + 4 * (lane & 7);
+            if (at < whole) copy16(to + 16 * j * kPitch, at);
+            p += 4 * step;
         }
-        e = first + lane * step;
-        const int64_t at = (e & ~int64_t(3)) + 32;
-        if ((e & 3) && at < whole) copy16(dst - 4 * ((lane >> 3) * kPitch + 4 * (lane & 7)) + 4 * (lane * kPitch + 32), base + at);
+        p = piece(lane);
+        const float* at = boundary(p) + 32;
+        if (place(p) && at < whole) copy16(dst + 4 * (lane * kPitch + 32), at);
     }
 };
 
@@ -189,31 +202,51 @@ __device__ __forceinline__ void read_raw(float (&v)[16], const uint8_t* raw, int
 }
 
 // The same of a slice that came in pieces: values from K on are zero (A's are too, but what lies there may be NaN).
-__device__ __forceinline__ void read_pieces(float (&v)[16], const uint8_t* raw, const Operand& o, const Pieces& p, int ks, int h, int lane) {
-    const float* q = reinterpret_cast<const float*>(raw);
-    const int64_t whole = p.total & ~int64_t(3);
-    if (o.layout == kCols) {
-        const int64_t e = p.first + lane + 16 * h * p.step;   // this thread's first value
-        const uint32_t at = uint32_t(p.first + 16 * h * p.step), step = uint32_t(p.step);
+__device__ __forceinline__ void read_pieces(float (&v)[16], const uint8_t* raw, int layout, const Pieces& p, int ks, int h, int lane) {
+    if (layout == kCols) {
+        const float* q = reinterpret_cast<const float*>(raw) + 16 * h * kPitch + lane;
+        uint32_t at = Pieces::place(p.piece(16 * h));
 #pragma unroll
-        for (int x = 0; x < 16; ++x) v[x] = q[(16 * h + x) * kPitch + ((at + x * step) & 3) + lane];
-        if (16 * h + 16 > ks || e + 15 * p.step >= whole) {
-#pragma unroll
+        for (int x = 0; x < 16; ++x) {
+            v[x] = q[x * kPitch + (at & 3)];
+            at += p.step;
+        }
+        const float* e = p.piece(16 * h) + lane;   // this thread's first value
+        if (16 * h + 16 > ks || e + 15 * uint64_t(p.step) >= p.whole) {
+#pragma unroll 1
             for (int x = 0; x < 16; ++x) {
-                if (16 * h + x >= ks) v[x] = 0.f;
-                else if (e + x * p.step >= whole) v[x] = e + x * p.step < p.total ? load1(o.base + e + x * p.step) : 0.f;
+                const float* y = e + x * uint64_t(p.step);
+                const float z = 16 * h + x >= ks || y >= p.end ? 0.f : load1(y);
+                if (16 * h + x >= ks || y >= p.whole) {
+#pragma unroll
+                    for (int u = 0; u < 16; ++u)
+                        if (u == x) v[u] = z;
+                }
             }
         }
     } else {
-        const int64_t e = p.first + lane * p.step;
-        const float* r = q + lane * kPitch + (uint32_t(e) & 3) + 16 * h;
+        // this lane's piece: five 16-byte parts (8 lanes' parts lie in different banks), moved down by its place
+        const float* e = p.piece(lane);
+        const uint32_t place = Pieces::place(e);
+        float w[20];
 #pragma unroll
-        for (int x = 0; x < 16; ++x) v[x] = r[x];
-        if (16 * h + 16 > ks || e + 16 * h + 15 >= whole) {
+        for (int u = 0; u < 5; ++u) {
+            const float4 f = *reinterpret_cast<const float4*>(raw + 4 * (lane * kPitch + 16 * h + 4 * u));
+            w[4 * u] = f.x;
+            w[4 * u + 1] = f.y;
+            w[4 * u + 2] = f.z;
+            w[4 * u + 3] = f.w;
+        }
+#pragma unroll
+        for (int x = 0; x < 18; ++x) w[x] = place & 2 ? w[x + 2] : w[x];
+#pragma unroll
+        for (int x = 0; x < 16; ++x) v[x] = place & 1 ? w[x + 1] : w[x];
+        e += 16 * h;
+        if (16 * h + 16 > ks || e + 15 >= p.whole) {
 #pragma unroll
             for (int x = 0; x < 16; ++x) {
                 if (16 * h + x >= ks) v[x] = 0.f;
-                else if (e + 16 * h + x >= whole) v[x] = e + 16 * h + x < p.total ? load1(o.base + e + 16 * h + x) : 0.f;
+                else if (e + x >= p.whole) v[x] = e + x < p.end ? load1(e + x) : 0.f;
             }
         }
     }
@@ -362,6 +395,14 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
                 const CUtensorMap *ma = w.set ? &maps.a[1] : &maps.a[0], *mb = w.set ? &maps.b[1] : &maps.b[0];
                 for (int kk = 0; kk < nk; ++kk, ++g) {
                     const int s = g % kStages, ph = g / kStages, k0 = kk * kBK;
+                    // a stage is refilled as soon as it is read, which leaves no time for memory's latency: the slice
+                    // after the stages' comes into L2 meanwhile
+                    if (kk + kStages < nk && ptx::elect_one()) {
+                        const int k1 = k0 + kStages * kBK;
+                        prefetch_3d(ma, la == kCols ? w.m0 : k1, la == kCols ? k1 : w.m0, w.batch);
+                        if (tma_b) prefetch_3d(mb, lb == kCols ? w.n0 : k1, lb == kCols ? k1 : w.n0, w.batch);
+                    }
+                    __syncwarp();
                     if (!warp_wait(&B.raw_empty[s], (ph & 1) ^ 1, abort_flag, tmo)) {
                         stop = true;
                         break;
@@ -475,13 +516,12 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
             kk -= nk;
             t += gridDim.x;
         }
-        const auto copy_b = [&](int t, int kk) {
-            const Tile w(a, t);
+        const auto pieces_of = [&](const Tile& w, int kk) {
             const Operand& o = w.set ? a.set[1].b : a.set[0].b;
-            Pieces(o, w.batch, w.n0 + (i & 96), kk * kBK, a.nb).copy(ptx::smem_addr(my_raw), o.base, lane);
+            return Pieces(o, w.batch, w.n0 + (i & 96), kk * kBK, a.nb);
         };
-        if (pieces && t < a.n_tiles) copy_b(t, kk);
-        Tile w(a, t);
+        Tile w(a, t), ahead = w;
+        if (pieces && t < a.n_tiles) pieces_of(w, kk).copy(ptx::smem_addr(my_raw), lane);
         while (t < a.n_tiles) {
             const Operand& ob = w.set ? a.set[1].b : a.set[0].b;
             const int la = w.set ? a.set[1].a.layout : a.set[0].a.layout;
@@ -490,6 +530,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
                 next_kk -= nk;
                 next += gridDim.x;
             }
+            if (next != t) ahead = Tile(a, next);
             if (!warp_wait(&B.raw_full[s], use & 1, abort_flag, tmo) ||
                 !warp_wait(&B.empty[s], (use & 1) ^ 1, abort_flag, tmo))
                 break;
@@ -497,15 +538,15 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
             if (pieces) {
                 asm volatile("cp.async.wait_all;" ::: "memory");
                 __syncwarp();
-                const Pieces p(ob, w.batch, w.n0 + (i & 96), kk * kBK, a.nb);
+                const Pieces p = pieces_of(w, kk);
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     float v[16];
-                    read_pieces(v, my_raw, ob, p, a.K - kk * kBK, h, lane);
+                    read_pieces(v, my_raw, ob.layout, p, a.K - kk * kBK, h, lane);
                     store_b(v, stage_b, h, i);
                 }
                 __syncwarp();  // every lane has read the pieces
-                if (next < a.n_tiles) copy_b(next, next_kk);
+                if (next < a.n_tiles) pieces_of(ahead, next_kk).copy(ptx::smem_addr(my_raw), lane);
             } else {
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
@@ -527,7 +568,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
             ptx::tc_fence_before();
             __syncwarp();
             if (lane == 0) ptx::mbar_arrive(&B.full[s]);
-            if (next != t) w = Tile(a, next);
+            w = ahead;
             t = next;
             kk = next_kk;
             ++use;
