@@ -424,7 +424,8 @@ int veda_attend_int8_paired(const veda_layout* layout, const void* q_codes, cons
  *
  * All sums are fp32 or wider, nothing is atomic, and two calls on the same inputs give the same bits.
  * Limits of every call here: 16384 video tiles and 65535 heads (VEDA_ERR_UNSUPPORTED beyond). Buffers need
- * 16-byte alignment. Workspaces are caller-owned scratch, overwritten by the call and free for other use once
+ * 16-byte alignment. The first call that uses a layout on a device uploads its index data (an allocation and a copy
+ * that waits): make it before any stream capture. Workspaces are caller-owned scratch, overwritten by the call and free for other use once
  * its kernels have finished; two calls that may overlap need two. */
 
 /* The teacher's tile logits: full attention's logits, max-pooled over every pair of video tiles,
@@ -459,7 +460,8 @@ int veda_bias_index(const veda_layout* layout, const veda_bias_spec* spec, int32
 /* veda_score's logits with the bias of each pair's bucket added,
  *     scores[h, i, j] = q_hat_i . k_hat_j / sqrt(D) + bias[h, bucket(i, j)],
  * keeping the projected features for veda_score_backward.
- *  spec, bias  the buckets, and device fp32 [n_heads, buckets]; both NULL: no bias.
+ *  spec, bias  the buckets, and device fp32 [n_heads, buckets]; both NULL: no bias. -inf keeps a bucket's pairs from
+ *              being selected; finite values are taken no larger than 2^120 in magnitude.
  *  hats        device fp32 [2, n_heads, n_video, D] out: q_hat, then k_hat.
  *  workspace   at least veda_score_bias_workspace_bytes().
  * Other arguments and errors as veda_score. */
@@ -486,13 +488,14 @@ int veda_bias_backward(const veda_layout* layout, const float* d_scores, int32_t
  *  t_cnt       device int32 [n_heads, n_video]: entries of each list, at most width.
  *  t_val       the teacher's logits: device fp32 [n_heads, n_video, width], one per entry of t_idx, or with
  *              by_column != 0 [n_heads, n_video, n_video] (veda_teacher's output), read at the listed columns.
- *  tau         temperature, > 0.
+ *  tau         temperature, in [1e-30, 1e30].
  *  row_weight  device fp32 [n_heads, n_video], or NULL for 1: w, for instance 1 / rows for a mean.
  *  loss        device fp32 [n_heads, n_video] out.
  *  d_scores    device fp32 [n_heads, n_video, n_video] out, or NULL for the loss alone; must not overlap scores.
  * A row without a target (an empty list, or -inf at every entry of it) or without a score above -inf gets loss 0
  * and gradient 0. A listed -inf carries no mass; a score of -inf has q = 0, and loss +inf where the teacher has
- * mass there. NaN, and +inf scores, give NaN in their row. A list that is not ascending, leaves [0, n_tiles) or is longer than width
+ * mass there. A NaN or +inf score gives a NaN loss and NaN gradients in its row, a NaN or +inf teacher logit a NaN loss
+ * and NaN at the listed columns. A list that is not ascending, leaves [0, n_tiles) or is longer than width
  * is cut at its first bad entry, and veda_sync_status reports VEDA_ERR_BAD_LIST. */
 int veda_distill(const veda_layout* layout, const float* scores, int32_t n_heads, const int32_t* t_idx,
                  const float* t_val, const int32_t* t_cnt, int32_t width, int32_t by_column, float tau,

@@ -5,9 +5,10 @@
 // Each fp32 operand is split into two tf32 parts, x = hi + lo, and a b is taken as hi_a hi_b + hi_a lo_b +
 // lo_a hi_b (what is left out is under 1.25 x 2^-20 |a b|; score.cuh has the bound). What keeps the sums at
 // the level of fp32 rounding as well: the tensor core truncates when it adds into its accumulator, so the errors of a
-// long sum all have one sign and add up (one accumulator over K = 384 and three products loses 1.4e-6, measured;
-// rounded fp32 sums lose 2e-7). So the sums are cut every kChunk values of K, and the epilogue warps add the chunks
-// in registers in rounded fp32; and each slice's small products go first, into an accumulator that is still small.
+// long sum all have one sign and add up. So the sums are cut at every slice of 32 values of K, and the epilogue warps add
+// the slices' sums in registers in rounded fp32; and a slice's small products go first, into an accumulator that is still
+// small. Scores of 819 tiles, 24 heads against 64 bits: 3.9e-6 with one accumulator, 1.0e-6 with sums of 64 values, 3.4e-7
+// with these (97 us instead of 95); fp32 products leave 5.4e-7.
 //
 // Both operands need the split, and it is shared memory that bounds the kernel (with both parts of both operands in
 // shared memory an MMA of 128 x 128 x 8 takes 117 cycles instead of 64, measured). So A, whose row a thread can hold, goes
@@ -48,7 +49,7 @@
 namespace veda {
 namespace train {
 
-constexpr int kBM = 128, kBN = 128, kBK = 32, kChunk = 64;
+constexpr int kBM = 128, kBN = 128, kBK = 32;
 constexpr int kPart = 128 * kBK * 4;    // 16 KB: one 128-row slice of an operand, raw or one part of it
 constexpr int kStageBytes = 2 * kPart;  // B hi, B lo
 constexpr int kStages = 3;              // of the raw slices (A, B) and of their parts; a split group has one of each
@@ -314,7 +315,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(&B + 1);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int nk = (a.K + kBK - 1) / kBK, nc = (a.K + kChunk - 1) / kChunk;
+    const int nk = (a.K + kBK - 1) / kBK;
     const uint64_t tmo = a.timeout_ns;
 
     if (threadIdx.x == 0) {
@@ -347,13 +348,12 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
         if (warp == 0) {
             // ------------------------------------------------------------------------ MMA issuer
             constexpr uint32_t kId = tf32x3::idesc(kBM, kBN);
-            int g = 0, gc = 0;  // slices and chunks consumed
+            int g = 0;  // slices consumed
             bool stop = false;
             for (int t = blockIdx.x; t < a.n_tiles && !stop; t += gridDim.x) {
                 for (int kk = 0; kk < nk; ++kk, ++g) {
-                    const int s = g % kStages, b = gc & 1;
-                    const bool first = kk % (kChunk / kBK) == 0;
-                    if ((first && !warp_wait(&B.acc_empty[b], ((gc >> 1) & 1) ^ 1, abort_flag, tmo)) ||
+                    const int s = g % kStages, b = g & 1;
+                    if (!warp_wait(&B.acc_empty[b], ((g >> 1) & 1) ^ 1, abort_flag, tmo) ||
                         !warp_wait(&B.full[s], (g / kStages) & 1, abort_flag, tmo)) {
                         stop = true;
                         break;
@@ -366,16 +366,13 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
                     // 8 tf32 = 32 bytes of B per k-step (2 of the descriptor's 16-byte units), 8 columns of A
 #pragma unroll
                     for (int k8 = 0; k8 < kBK / 8; ++k8) {
-                        mma_ts(d, ah + 32 + 8 * k8, bh + uint64_t(2 * k8), kId, first && k8 == 0 ? 0u : 1u);
+                        mma_ts(d, ah + 32 + 8 * k8, bh + uint64_t(2 * k8), kId, k8 > 0 ? 1u : 0u);
                         mma_ts(d, ah + 8 * k8, bl + uint64_t(2 * k8), kId, 1u);
                     }
 #pragma unroll
                     for (int k8 = 0; k8 < kBK / 8; ++k8) mma_ts(d, ah + 8 * k8, bh + uint64_t(2 * k8), kId, 1u);
                     ptx::mma_commit_w(&B.empty[s]);
-                    if (kk % (kChunk / kBK) == kChunk / kBK - 1 || kk == nk - 1) {
-                        ptx::mma_commit_w(&B.acc_full[b]);
-                        ++gc;
-                    }
+                    ptx::mma_commit_w(&B.acc_full[b]);
                 }
             }
             // every product issued must be complete before the TMEM is released
@@ -433,7 +430,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
         // ---------------------------------------------------------------------------- epilogue
         ptx::regs_inc<88>();
         const int q = warp & 3, half = (warp - 4) >> 2;  // TMEM lane quarter (m 32 q ..), columns 64 half ..
-        int gc = 0;
+        int g = 0;
         bool stop = false;
         for (int t = blockIdx.x; t < a.n_tiles && !stop; t += gridDim.x) {
             const Tile w(a, t);
@@ -477,9 +474,9 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
                     for (int e = 0; e < 16; ++e) acc[j + e] += __uint_as_float(x[e]);
                 }
             };
-            for (int c = 0; c < nc; ++c, ++gc) {
-                const int b = gc & 1;
-                if (!warp_wait(&B.acc_full[b], (gc >> 1) & 1, abort_flag, tmo)) {
+            for (int kk = 0; kk < nk; ++kk, ++g) {
+                const int b = g & 1;
+                if (!warp_wait(&B.acc_full[b], (g >> 1) & 1, abort_flag, tmo)) {
                     stop = true;
                     break;
                 }

@@ -173,7 +173,9 @@ int bias_chunks(int n, int n_heads) {
 
 constexpr int kBiasMaxSmem = 227 * 1024;
 // one or two sets of sums, the warps' cross-span sums, and a query of 8 bytes per row
-size_t bias_smem(int per, int offsets, int rows) { return ((per <= 2 ? 2 : 1) * size_t(offsets) + 32 + 1) / 2 * 8 + size_t(rows) * 8; }
+size_t bias_smem(const BiasBackwardArgs& a) {
+    return ((a.n <= 1024 ? 2 : 1) * size_t(a.offsets) + 32 + 1) / 2 * 8 + size_t(a.rows_per_chunk) * 8;
+}
 
 template <int kPer, bool kOneSpan>
 int launch_bias_backward(const BiasBackwardArgs& a, int chunks, int n_heads, const DeviceInfo& di, cudaStream_t s) {
@@ -185,7 +187,7 @@ int launch_bias_backward(const BiasBackwardArgs& a, int chunks, int n_heads, con
         set[di.ordinal].store(true);
     }
     const int threads = std::max(128, ((a.n + kPer - 1) / kPer + 31) / 32 * 32);
-    bias_backward_kernel<kPer, kOneSpan><<<dim3(chunks, n_heads), threads, bias_smem(kPer, a.offsets, a.rows_per_chunk), s>>>(a);
+    bias_backward_kernel<kPer, kOneSpan><<<dim3(chunks, n_heads), threads, bias_smem(a), s>>>(a);
     return launch_status("bias_backward_kernel");
 }
 
@@ -372,7 +374,7 @@ extern "C" int veda_bias_backward(const veda_layout* layout, const float* d_scor
         const int chunks = bias_chunks(a.n, n_heads);
         cudaStream_t s = static_cast<cudaStream_t>(stream);
         int rc;
-        if (bias_smem(a.n <= 1024 ? 2 : 4, a.offsets, a.rows_per_chunk) > size_t(kBiasMaxSmem) || a.n > 8192) {
+        if (bias_smem(a) > size_t(kBiasMaxSmem) || a.n > 8192) {
             const int smem = a.n * int(sizeof(float));
             cudaError_t e = cudaFuncSetAttribute(bias_backward_wide_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
             if (e != cudaSuccess)
@@ -410,8 +412,7 @@ extern "C" int veda_distill(const veda_layout* layout, const float* scores, int3
         clear_error();
         if (!layout || !scores || !t_idx || !t_val || !t_cnt || !loss) return fail(VEDA_ERR_INVALID, "veda_distill: NULL argument");
         if (n_heads <= 0 || width <= 0) return fail(VEDA_ERR_INVALID, "veda_distill: n_heads and width must be positive");
-        if (!(tau > 0.f) || !std::isfinite(tau) || !std::isfinite(1.f / tau))
-            return fail(VEDA_ERR_INVALID, "veda_distill: tau must be positive and finite, and so its inverse");
+        if (!(tau >= 1e-30f && tau <= 1e30f)) return fail(VEDA_ERR_INVALID, "veda_distill: tau must lie in [1e-30, 1e30]");
         for (const void* p : {(const void*)scores, (const void*)t_idx, (const void*)t_val, (const void*)t_cnt,
                               (const void*)row_weight, (const void*)loss, (const void*)d_scores})
             if (!aligned16(p)) return fail(VEDA_ERR_INVALID, "veda_distill: buffers need 16-byte alignment");

@@ -157,6 +157,25 @@ def test_score_bias(geo, dim, heads, reach, far):
     within(out, want, tol + 4 * EPS * want.abs())
 
 
+@pytest.mark.parametrize("dim", [64, 128])
+def test_score_bias_masks(dim):
+    # -inf and the type's lowest value in buckets: the first leaves -inf, the second a finite score below all others
+    geo, reach, far = Geometry(**GEOMETRIES["refs"]), (3, 3, 3), (8, 8, 8)
+    n, low = geo.n, torch.finfo(torch.float32).min
+    total = L.veda_bias_buckets(reach, far)
+    bias = torch.zeros(1, total, device=DEV)
+    bias[0, ::3], bias[0, 1::3], bias[0, -1] = -math.inf, low, 3e38
+    fq, fk, pq, pk = feats(1, 1, n, dim), feats(4, 1, n, dim), projections(7, 1, dim), projections(8, 1, dim)
+    out, _ = score_bias(geo, fq, fk, pq, pk, reach, far, bias)
+    plain, _ = score_bias(geo, fq, fk, pq, pk)
+    kind = bias[0][torch.as_tensor(L.veda_bias_index(geo.layout, reach, far), device=DEV).long()][None]
+    assert bool((out[kind == -math.inf] == -math.inf).all())
+    for value, sign in ((low, -1.0), (3e38, 1.0)):
+        got = out[kind == value].double()
+        assert bool(((got - sign * 2.0 ** 120).abs() <= 4 * EPS * 2.0 ** 120).all())
+    assert float((out - plain)[kind == 0].abs().max()) <= 8 * EPS * float(plain.abs().max())
+
+
 # ------------------------------------------------------------------------------------------- bias gradient
 
 

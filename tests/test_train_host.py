@@ -120,6 +120,7 @@ def test_c_entries_refuse_bad_arguments_before_any_device():
         lib.veda_distill(h, ok, 2, ok, ok, ok, 8, 0, float("nan"), None, ok, d, None),
         lib.veda_distill(h, ok, 2, ok, ok, ok, 8, 0, float("inf"), None, ok, d, None),
         lib.veda_distill(h, ok, 2, ok, ok, ok, 8, 0, 1e-40, None, ok, d, None),
+        lib.veda_distill(h, ok, 2, ok, ok, ok, 8, 0, 2e30, None, ok, d, None),
         lib.veda_distill(h, ok, 2, ok, ok, ok, 8, 0, 1.0, None, ok, ok + 16, None),  # overlaps scores
         lib.veda_distill(h, ok, 2, ok, ok, None, 8, 0, 1.0, None, ok, d, None),
         lib.veda_score_backward(h, ok, ok, 2, 64, ok, ok, ok, ok, ok, 4, None),
