@@ -28,11 +28,12 @@
 //                the 128-byte swizzle, so that 8 lanes' 16-byte pieces fall into 8 different banks; columns are
 //                neighbours for neighbouring lanes), and writes A's parts to its TMEM lane and B's in the swizzle that
 //                the MMA reads.
-// A score gradient whose row length is no multiple of 16 bytes has no tensor map: the split warps copy its slices themselves,
-// a turn ahead. Each warp copies what its own lanes read, 32 pieces of 32 values, from the 16-byte boundary before each
-// piece (up to three values early and late, inside the tensor), and reads them at the remainder. The tensor's last one
-// to three values, when they fill no 16 bytes, are read from global memory. (The gradient of 819-tile scores took 275 us
-// with values copied one by one, 340 with a bulk copy per piece, 154 with the copies in warps of their own.)
+// A score gradient whose row length n is no multiple of four values has no tensor map of its own: its rows start off the
+// 16-byte boundaries. But every fourth row does have one, with a stride of 4 n values, from the boundary before its first
+// value: four maps, one for each remainder b of the row's number (over all batches), in which row 4 a + b begins at
+// place (b n) % 4. A slice is four boxes, one value quad wider and one row higher than its share; a thread reads its
+// values at their places. (The gradient of 819-tile scores, both kernels: 275 us with values copied one by one, 340 with
+// a bulk copy per piece of a row, 127 with 16-byte copies by the split warps.)
 // Every wait is bounded; a CTA that gives up lets its MMAs finish, frees its TMEM and returns.
 #pragma once
 
@@ -53,8 +54,11 @@ constexpr int kBM = 128, kBN = 128, kBK = 32;
 constexpr int kPart = 128 * kBK * 4;    // 16 KB: one 128-row slice of an operand, raw or one part of it
 constexpr int kStageBytes = 2 * kPart;  // B hi, B lo
 constexpr int kStages = 3;              // of the raw slices (A, B) and of their parts; a split group has one of each
-constexpr int kPitch = 36;              // floats a copied piece of 32 values may take
-constexpr int kRawB = 128 * kPitch * 4; // 18 KB: 32 pieces for each of a group's four warps (a tensor-map slice takes less)
+constexpr int kQuadRows = 33, kQuadWidth = 36;   // a box of a quarter of 128 rows x 32 K (kRows) ...
+constexpr int kQuadK = 9, kQuadCols = 132;       // ... and of 32 K x 128 rows (kCols), in rows and values
+constexpr int kQuadBytes = kQuadRows * kQuadWidth * 4, kQuadStep = 4864;  // boxes lie on 128-byte boundaries
+static_assert(kQuadBytes == kQuadK * kQuadCols * 4 && kQuadBytes <= kQuadStep && kQuadStep % 128 == 0, "boxes of one size");
+constexpr int kRawB = 4 * kQuadStep;      // 19 KB (a slice of a dense map takes 16)
 constexpr int kRawBytes = kPart + kRawB;  // A, B
 constexpr int kOffRaw = kStages * kStageBytes;
 constexpr int kOffBar = kOffRaw + kStages * kRawBytes;
@@ -88,11 +92,12 @@ struct Operand {
     int64_t stride;
     int rows;
     int layout;
-    int tma;         // 0: no tensor map, copied in pieces (B only, and of all sets or none)
+    int dense;       // one tensor map; 0: four, one for every fourth row (B only)
 };
 
 struct Maps {
-    CUtensorMap a[2], b[2];  // boxes of 32 K x 128 rows, 128-byte swizzle (kRows), or 128 rows x 32 K (kCols)
+    CUtensorMap a[2];     // boxes of 32 K x 128 rows, 128-byte swizzle (kRows), or 128 rows x 32 K (kCols)
+    CUtensorMap b[2][4];  // the same in b[set][0], or every fourth row's in boxes of kQuadWidth x kQuadRows or kQuadCols x kQuadK
 };
 
 struct Set {
@@ -143,47 +148,6 @@ __device__ __forceinline__ void prefetch_3d(const void* desc, int32_t c0, int32_
                  : "memory");
 }
 
-// sixteen bytes global -> shared in the background
-__device__ __forceinline__ void copy16(uint32_t dst, const float* src) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
-
-// A warp's pieces of a slice of an operand without a tensor map: its 32 rows (kRows), or its 32 columns of every k (kCols).
-struct Pieces {
-    const float* first;   // element (the warp's first row, k0)
-    const float* whole;   // the tensor's end, less what fills no 16 bytes
-    const float* end;
-    uint32_t step;        // elements between pieces: a row, or a k
-    __device__ __forceinline__ Pieces(const Operand& o, int batch, int r0, int k0, int nb) {
-        first = o.base + batch * o.batch + (o.layout == kCols ? int64_t(k0) * o.stride + r0 : int64_t(r0) * o.stride + k0);
-        end = o.base + nb * o.batch;
-        whole = o.base + ((nb * o.batch) & ~int64_t(3));
-        step = uint32_t(o.stride);
-    }
-    __device__ __forceinline__ const float* piece(int x) const { return first + uint32_t(x) * step; }
-    // the 16-byte boundary before p, and p's place behind it (the tensor's base is 16-byte aligned)
-    static __device__ __forceinline__ const float* boundary(const float* p) {
-        return reinterpret_cast<const float*>(reinterpret_cast<uintptr_t>(p) & ~uintptr_t(15));
-    }
-    static __device__ __forceinline__ uint32_t place(const float* p) { return (uint32_t(reinterpret_cast<uintptr_t>(p)) >> 2) & 3; }
-    // The warp copies 32 pieces of nine 16-byte parts: eight parts of four pieces at a time, then the ninth of all (needed
-    // only where a piece starts past its boundary). Parts that are not whole inside the tensor are left out; pieces past
-    // the operand's rows or K hold other values of the tensor, which nothing uses.
-    __device__ __forceinline__ void copy(uint32_t dst, int lane) const {
-        const uint32_t to = dst + 4 * ((lane >> 3) * kPitch + 4 * (lane & 7));
-        const float* p = piece(lane >> 3);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const float* at = boundary(p) + 4 * (lane & 7);
-            if (at < whole) copy16(to + 16 * j * kPitch, at);
-            p += 4 * step;
-        }
-        p = piece(lane);
-        const float* at = boundary(p) + 32;
-        if (place(p) && at < whole) copy16(dst + 4 * (lane * kPitch + 32), at);
-    }
-};
-
 // Half h of this thread's row of a raw slice (row i, K from 16 h).
 __device__ __forceinline__ void read_raw(float (&v)[16], const uint8_t* raw, int layout, int h, int i) {
     if (layout == kCols) {
@@ -202,54 +166,31 @@ __device__ __forceinline__ void read_raw(float (&v)[16], const uint8_t* raw, int
     }
 }
 
-// The same of a slice that came in pieces: values from K on are zero (A's are too, but what lies there may be NaN).
-__device__ __forceinline__ void read_pieces(float (&v)[16], const uint8_t* raw, int layout, const Pieces& p, int ks, int h, int lane) {
+// The same of a slice of four boxes. `first`: the number over all batches of the slice's first row (kRows), or of its first
+// k (kCols); n the row length; values from ks on are zero (with kCols a k past the operand's is the next batch's row).
+// Neighbouring lanes read neighbouring banks: with kRows four rows share a bank group and begin at four different places.
+__device__ __forceinline__ void read_quads(float (&v)[16], const uint8_t* raw, int layout, int first, int n, int ks, int h, int i) {
+    const float* q = reinterpret_cast<const float*>(raw);
+    constexpr int kStep = kQuadStep / 4;
     if (layout == kCols) {
-        const float* q = reinterpret_cast<const float*>(raw) + 16 * h * kPitch + lane;
-        uint32_t at = Pieces::place(p.piece(16 * h));
+        const float* p[4];
 #pragma unroll
-        for (int x = 0; x < 16; ++x) {
-            v[x] = q[x * kPitch + (at & 3)];
-            at += p.step;
+        for (int j = 0; j < 4; ++j) {
+            const int x = (first & 3) + j, b = x & 3;
+            p[j] = q + b * kStep + ((b * n) & 3) + (x >> 2) * kQuadCols + i;
         }
-        const float* e = p.piece(16 * h) + lane;   // this thread's first value
-        if (16 * h + 16 > ks || e + 15 * uint64_t(p.step) >= p.whole) {
-#pragma unroll 1
-            for (int x = 0; x < 16; ++x) {
-                const float* y = e + x * uint64_t(p.step);
-                const float z = 16 * h + x >= ks || y >= p.end ? 0.f : load1(y);
-                if (16 * h + x >= ks || y >= p.whole) {
 #pragma unroll
-                    for (int u = 0; u < 16; ++u)
-                        if (u == x) v[u] = z;
-                }
-            }
+        for (int x = 0; x < 16; ++x) v[x] = p[x & 3][(4 * h + (x >> 2)) * kQuadCols];
+        if (16 * h + 16 > ks) {
+#pragma unroll
+            for (int x = 0; x < 16; ++x)
+                if (16 * h + x >= ks) v[x] = 0.f;
         }
     } else {
-        // this lane's piece: five 16-byte parts (8 lanes' parts lie in different banks), moved down by its place
-        const float* e = p.piece(lane);
-        const uint32_t place = Pieces::place(e);
-        float w[20];
+        const int x = (first & 3) + i, b = x & 3;
+        const float* p = q + b * kStep + ((b * n) & 3) + (x >> 2) * kQuadWidth + 16 * h;
 #pragma unroll
-        for (int u = 0; u < 5; ++u) {
-            const float4 f = *reinterpret_cast<const float4*>(raw + 4 * (lane * kPitch + 16 * h + 4 * u));
-            w[4 * u] = f.x;
-            w[4 * u + 1] = f.y;
-            w[4 * u + 2] = f.z;
-            w[4 * u + 3] = f.w;
-        }
-#pragma unroll
-        for (int x = 0; x < 18; ++x) w[x] = place & 2 ? w[x + 2] : w[x];
-#pragma unroll
-        for (int x = 0; x < 16; ++x) v[x] = place & 1 ? w[x + 1] : w[x];
-        e += 16 * h;
-        if (16 * h + 16 > ks || e + 15 >= p.whole) {
-#pragma unroll
-            for (int x = 0; x < 16; ++x) {
-                if (16 * h + x >= ks) v[x] = 0.f;
-                else if (e + x >= p.whole) v[x] = e + x < p.end ? load1(e + x) : 0.f;
-            }
-        }
+        for (int x = 0; x < 16; ++x) v[x] = p[x];
     }
 }
 
@@ -388,8 +329,9 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
                 const Tile w(a, t);
                 const int la = w.set ? a.set[1].a.layout : a.set[0].a.layout;
                 const int lb = w.set ? a.set[1].b.layout : a.set[0].b.layout;
-                const int tma_b = w.set ? a.set[1].b.tma : a.set[0].b.tma;
-                const CUtensorMap *ma = w.set ? &maps.a[1] : &maps.a[0], *mb = w.set ? &maps.b[1] : &maps.b[0];
+                const int dense = w.set ? a.set[1].b.dense : a.set[0].b.dense;
+                const int row0 = w.batch * (lb == kCols ? a.K : a.N);  // the batch's first row, over all of them
+                const CUtensorMap *ma = w.set ? &maps.a[1] : &maps.a[0], *mb = w.set ? maps.b[1] : maps.b[0];
                 for (int kk = 0; kk < nk; ++kk, ++g) {
                     const int s = g % kStages, ph = g / kStages, k0 = kk * kBK;
                     // a stage is refilled as soon as it is read, which leaves no time for memory's latency: the slice
@@ -397,7 +339,12 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
                     if (kk + kStages < nk && ptx::elect_one()) {
                         const int k1 = k0 + kStages * kBK;
                         prefetch_3d(ma, la == kCols ? w.m0 : k1, la == kCols ? k1 : w.m0, w.batch);
-                        if (tma_b) prefetch_3d(mb, lb == kCols ? w.n0 : k1, lb == kCols ? k1 : w.n0, w.batch);
+                        if (dense) {
+                            prefetch_3d(mb, lb == kCols ? w.n0 : k1, lb == kCols ? k1 : w.n0, w.batch);
+                        } else {
+                            for (int b = 0; b < 4; ++b)
+                                prefetch_3d(mb + b, lb == kCols ? w.n0 : k1, (row0 + (lb == kCols ? k1 : w.n0)) >> 2, 0);
+                        }
                     }
                     __syncwarp();
                     if (!warp_wait(&B.raw_empty[s], (ph & 1) ^ 1, abort_flag, tmo)) {
@@ -406,12 +353,17 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
                     }
                     if (ptx::elect_one()) {
                         uint8_t* raw = smem + kOffRaw + s * kRawBytes;
-                        ptx::mbar_arrive_expect_tx(&B.raw_full[s], tma_b ? 2 * kPart : kPart);
+                        ptx::mbar_arrive_expect_tx(&B.raw_full[s], kPart + (dense ? kPart : 4 * kQuadBytes));
                         ptx::tma_load_3d_hint(raw, ma, la == kCols ? w.m0 : k0, la == kCols ? k0 : w.m0, w.batch,
                                               &B.raw_full[s], keep);
-                        if (tma_b)
+                        if (dense) {
                             ptx::tma_load_3d_hint(raw + kPart, mb, lb == kCols ? w.n0 : k0, lb == kCols ? k0 : w.n0, w.batch,
                                                   &B.raw_full[s], keep);
+                        } else {
+                            for (int b = 0; b < 4; ++b)
+                                ptx::tma_load_3d_hint(raw + kPart + b * kQuadStep, mb + b, lb == kCols ? w.n0 : k0,
+                                                      (row0 + (lb == kCols ? k0 : w.n0)) >> 2, 0, &B.raw_full[s], keep);
+                        }
                     }
                     __syncwarp();
                 }
@@ -505,20 +457,13 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
         const uint32_t stage_a = tmem + kStageA + uint32_t(64 * s) + (uint32_t(32 * (warp & 3)) << 16);
         uint8_t* stage_b = smem + s * kStageBytes;
         const uint8_t* raw = smem + kOffRaw + s * kRawBytes;
-        const bool pieces = !a.set[0].b.tma;
-        uint8_t* my_raw = smem + kOffRaw + s * kRawBytes + kPart + (warp & 3) * 32 * kPitch * 4;
         // this group's slices, every kStages-th of the CTA's sequence: tile t, slice kk, number `use` of the group
         int t = blockIdx.x, kk = s, use = 0;
         while (kk >= nk && t < a.n_tiles) {
             kk -= nk;
             t += gridDim.x;
         }
-        const auto pieces_of = [&](const Tile& w, int kk) {
-            const Operand& o = w.set ? a.set[1].b : a.set[0].b;
-            return Pieces(o, w.batch, w.n0 + (i & 96), kk * kBK, a.nb);
-        };
-        Tile w(a, t), ahead = w;
-        if (pieces && t < a.n_tiles) pieces_of(w, kk).copy(ptx::smem_addr(my_raw), lane);
+        Tile w(a, t);
         while (t < a.n_tiles) {
             const Operand& ob = w.set ? a.set[1].b : a.set[0].b;
             const int la = w.set ? a.set[1].a.layout : a.set[0].a.layout;
@@ -527,28 +472,23 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
                 next_kk -= nk;
                 next += gridDim.x;
             }
-            if (next != t) ahead = Tile(a, next);
             if (!warp_wait(&B.raw_full[s], use & 1, abort_flag, tmo) ||
                 !warp_wait(&B.empty[s], (use & 1) ^ 1, abort_flag, tmo))
                 break;
             ptx::tc_fence_after();
-            if (pieces) {
-                asm volatile("cp.async.wait_all;" ::: "memory");
-                __syncwarp();
-                const Pieces p = pieces_of(w, kk);
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    float v[16];
-                    read_pieces(v, my_raw, ob.layout, p, a.K - kk * kBK, h, lane);
-                    store_b(v, stage_b, h, i);
-                }
-                __syncwarp();  // every lane has read the pieces
-                if (next < a.n_tiles) pieces_of(ahead, next_kk).copy(ptx::smem_addr(my_raw), lane);
-            } else {
+            if (ob.dense) {
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     float v[16];
                     read_raw(v, raw + kPart, ob.layout, h, i);
+                    store_b(v, stage_b, h, i);
+                }
+            } else {
+                const int first = ob.layout == kCols ? w.batch * a.K + kk * kBK : w.batch * a.N + w.n0;
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    float v[16];
+                    read_quads(v, raw + kPart, ob.layout, first, int(ob.stride), a.K - kk * kBK, h, i);
                     store_b(v, stage_b, h, i);
                 }
             }
@@ -565,12 +505,11 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
             ptx::tc_fence_before();
             __syncwarp();
             if (lane == 0) ptx::mbar_arrive(&B.full[s]);
-            w = ahead;
+            if (next != t) w = Tile(a, next);
             t = next;
             kk = next_kk;
             ++use;
         }
-        asm volatile("cp.async.wait_all;" ::: "memory");
     }
 
     __syncthreads();

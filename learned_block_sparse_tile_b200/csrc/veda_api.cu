@@ -450,6 +450,24 @@ int make_f32_cols_map(CUtensorMap* m, const float* base, int64_t rows, int64_t K
     return VEDA_OK;
 }
 
+int make_f32_fourth_rows_map(CUtensorMap* m, const float* base, int64_t n, int64_t rows, int b, int width, int height) {
+    auto enc = tensor_map_encoder();
+    if (!enc) return fail(VEDA_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
+    if (b >= rows) b = 0;  // no such row: a map of some that exist, whose values nothing uses
+    const int64_t place = (b * n) & 3;
+    // (the third dimension has one element; a box's row ends at the row's end, so nothing past the matrix is read)
+    cuuint64_t gdim[3] = {cuuint64_t(n + place), cuuint64_t((rows - b + 3) / 4), 1};
+    cuuint64_t gstride[2] = {cuuint64_t(n) * 16, cuuint64_t(n) * 16 * gdim[1]};
+    cuuint32_t box[3] = {cuuint32_t(width), cuuint32_t(height), 1};
+    cuuint32_t estride[3] = {1, 1, 1};
+    CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, const_cast<float*>(base + b * n - place), gdim, gstride, box, estride,
+                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS)
+        return fail(VEDA_ERR_CUDA, "cuTensorMapEncodeTiled (every fourth row) failed (" + std::to_string(int(r)) + ")");
+    return VEDA_OK;
+}
+
 int launch_score_gemms(const float* feats_q, const float* feats_k, const float* proj_q, const float* proj_k, float* qh,
                        float* kh, float* pt_q, float* pt_k, float* scores, int nv, int dim, int n_heads,
                        cudaStream_t s) {

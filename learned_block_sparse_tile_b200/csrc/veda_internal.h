@@ -57,6 +57,9 @@ uint64_t wait_timeout_ns();
 int make_f32_map(CUtensorMap* m, const float* base, int64_t K, int64_t rows, int64_t batch);
 // the same over [batch][K][rows] (rows innermost): boxes of 128 rows x 32 K, not swizzled
 int make_f32_cols_map(CUtensorMap* m, const float* base, int64_t rows, int64_t K, int64_t batch);
+// the rows 4 a + b (a = 0, 1, ..) of a row-major fp32 [rows][n] matrix whose n need not be a multiple of four: row a of the map
+// begins at the 16-byte boundary before its first value, which lies at place (b n) % 4; boxes of width x height
+int make_f32_fourth_rows_map(CUtensorMap* m, const float* base, int64_t n, int64_t rows, int b, int width, int height);
 // TMA map over bf16 rows [rows, dim] in boxes of 128 rows x 64 columns with the 128-byte swizzle
 int make_bf16_rows_map(CUtensorMap* m, const void* base, int64_t rows, int dim);
 // `cudaGetLastError` after a launch, as a VEDA_* status

@@ -112,9 +112,17 @@ train::Operand operand(const float* base, int rows, int K, bool cols) {
     return {base, int64_t(rows) * K, stride, rows, cols ? train::kCols : train::kRows, stride % 4 == 0};
 }
 
-int operand_map(CUtensorMap* m, const train::Operand& o, int K, int batches) {
-    if (!o.tma) return VEDA_OK;
-    return o.layout == train::kCols ? make_f32_cols_map(m, o.base, o.rows, K, batches) : make_f32_map(m, o.base, K, o.rows, batches);
+// the operand's map, or its four
+int operand_maps(CUtensorMap* m, const train::Operand& o, int K, int batches) {
+    if (o.dense)
+        return o.layout == train::kCols ? make_f32_cols_map(m, o.base, o.rows, K, batches) : make_f32_map(m, o.base, K, o.rows, batches);
+    const int64_t rows = int64_t(batches) * (o.layout == train::kCols ? K : o.rows);
+    for (int b = 0; b < 4; ++b)
+        if (int rc = o.layout == train::kCols
+                         ? make_f32_fourth_rows_map(m + b, o.base, o.stride, rows, b, train::kQuadCols, train::kQuadK)
+                         : make_f32_fourth_rows_map(m + b, o.base, o.stride, rows, b, train::kQuadWidth, train::kQuadRows))
+            return rc;
+    return VEDA_OK;
 }
 
 // `after`: the launch before it on the stream is one of this call's, and its start may overlap that one's end
@@ -135,8 +143,8 @@ int launch_gemm(const char* what, train::Args a, const BiasExpand& expand, bool 
     a.err = di.err;
     train::Maps m{};
     for (int i = 0; i < a.n_sets; ++i) {
-        if (int rc = operand_map(&m.a[i], a.set[i].a, a.K, a.nb)) return rc;
-        if (int rc = operand_map(&m.b[i], a.set[i].b, a.K, a.nb)) return rc;
+        if (int rc = operand_maps(&m.a[i], a.set[i].a, a.K, a.nb)) return rc;
+        if (int rc = operand_maps(m.b[i], a.set[i].b, a.K, a.nb)) return rc;
     }
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(unsigned(std::min(a.n_tiles, di.sms)));

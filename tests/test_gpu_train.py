@@ -19,7 +19,10 @@ GEOMETRIES = {
     "ragged": dict(spans=[((3, 10, 12), (2, 8, 8))], text=200),                     # partial tiles, global tiles
     "refs": dict(spans=[((2, 16, 16), (2, 8, 8)), ((1, 9, 21), (1, 8, 16)), ((6, 16, 24), (8, 4, 4))], text=150, gap=3),
     "wide": dict(spans=[((5, 45, 50), (1, 8, 16))], text=1),                        # 120 tiles of odd fill
-    "over128": dict(spans=[((13, 24, 44), (2, 8, 8))]),                             # 126 tiles and more: two MMA tiles
+    "odd135": dict(spans=[((15, 24, 42), (1, 8, 16))]),                             # just over one MMA tile, an odd number
+    "even150": dict(spans=[((5, 45, 80), (1, 8, 16))]),                             # 150 = 2 modulo 4
+    "odd259": dict(spans=[((37, 8, 112), (1, 8, 16))], text=40),                    # three MMA tiles, 3 modulo 4
+    "quad260": dict(spans=[((65, 8, 60), (1, 8, 16))]),                             # rows of whole 16-byte pieces
     "line": dict(spans=[((259, 1, 3), (128, 1, 1))]),                               # boxes longer than the grid is
 }
 
