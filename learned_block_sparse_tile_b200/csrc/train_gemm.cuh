@@ -1,5 +1,5 @@
 // fp32 products of the predictor's scores and of their gradients on the tensor cores:
-//     C[batch][n][m] = scale sum_k A[batch](m, k) B[batch](n, k)  (+ a residual, or + the relative position bias),
+//     C[batch][n][m] = scale sum_k A[batch](m, k) B[batch](n, k)  (+ the relative position bias),
 // the operands read where they are, in any of three layouts (no transposed copies).
 //
 // Each fp32 operand is split into two tf32 parts, x = hi + lo, and a b is taken as hi_a hi_b + hi_a lo_b +
@@ -9,6 +9,9 @@
 // the slices' sums in registers in rounded fp32; and a slice's small products go first, into an accumulator that is still
 // small. Scores of 819 tiles, 24 heads against 64 bits: 3.9e-6 with one accumulator, 1.0e-6 with sums of 64 values, 3.4e-7
 // with these (97 us instead of 95); fp32 products leave 5.4e-7.
+//
+// The projections' residual, feats @ P + feats[:, :D] = feats @ (P + E) with E the identity in P's first D rows, is added to
+// A as it is split.
 //
 // Both operands need the split, and it is shared memory that bounds the kernel (with both parts of both operands in
 // shared memory an MMA of 128 x 128 x 8 takes 117 cycles instead of 64, measured). So A, whose row a thread can hold, goes
@@ -102,8 +105,7 @@ struct Maps {
 
 struct Set {
     Operand a, b;
-    float* C;               // [batch][N][M]
-    const float* residual;  // element (n, m) at batch * residual_batch + n * residual_stride + m, or null
+    float* C;  // [batch][N][M]
 };
 
 struct Args {
@@ -112,7 +114,7 @@ struct Args {
     int M, N, K;
     int tiles_m, tiles_n, n_tiles;
     float scale;
-    int64_t residual_batch, residual_stride;
+    int identity;           // A(m, m) + 1 in the place of A(m, m)
     // the bias of score tiles (table null: none), m the key and n the query: scale table[batch][key number + query number]
     const float* table;
     const int4* tile_num;
@@ -389,8 +391,6 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
             const uint32_t lanes = tmem + (uint32_t(32 * q) << 16) + uint32_t(64 * half);
             const int m = w.m0 + 32 * q + lane, mm = min(m, a.M - 1), n0 = w.n0 + 64 * half;
             const int left = a.N - n0;
-            // (selects, not a.set[w.set]: a runtime index into the kernel arguments would copy them to the stack)
-            const float* res = w.set ? a.set[1].residual : a.set[0].residual;
             float acc[64];  // what is added to the product, over its scale, then the sums; loads from clamped places
             if (a.table) {
                 const float* table = a.table + w.batch * a.table_stride;
@@ -408,10 +408,6 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
                         acc[j + x] = load1(table + o);
                     }
                 }
-            } else if (res) {
-                res += w.batch * a.residual_batch + mm;
-#pragma unroll
-                for (int x = 0; x < 64; ++x) acc[x] = load1(res + min(n0 + x, a.N - 1) * a.residual_stride);
             } else {
 #pragma unroll
                 for (int x = 0; x < 64; ++x) acc[x] = 0.f;
@@ -439,6 +435,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
             }
             if (stop) break;
             if (m < a.M) {
+                // (a select, not a.set[w.set]: a runtime index into the kernel arguments would copy them to the stack)
                 float* C = (w.set ? a.set[1].C : a.set[0].C) + int64_t(w.batch) * a.M * a.N + int64_t(n0) * a.M + m;
                 if (left >= 64) {
 #pragma unroll
@@ -496,6 +493,11 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
             for (int h = 0; h < 2; ++h) {
                 float v[16];
                 read_raw(v, raw, la, h, i);
+                if (a.identity && kk * kBK < a.M) {
+                    const int one = w.m0 + i - kk * kBK - 16 * h;
+#pragma unroll
+                    for (int x = 0; x < 16; ++x) v[x] += x == one ? 1.f : 0.f;
+                }
                 store_a(v, stage_a + 16 * h);
             }
             __syncwarp();

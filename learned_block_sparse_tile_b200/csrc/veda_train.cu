@@ -313,7 +313,7 @@ extern "C" int veda_score_bias(const veda_layout* layout, const float* feats_q, 
         if (bias)
             expand = {bias, table, float(std::sqrt(double(dim))), reinterpret_cast<const int4*>(dc->span_grid),
                       int(layout->span_grid.size() / 4), offsets, n_heads, b};
-        const int64_t nf = int64_t(n) * 3 * dim, nd = int64_t(n) * dim;
+        const int64_t nd = int64_t(n) * dim;
         // hats[tile][d], both sides in one launch, then scores[query][key]
         train::Args p{};
         p.n_sets = 2;
@@ -322,12 +322,11 @@ extern "C" int veda_score_bias(const veda_layout* layout, const float* feats_q, 
         p.N = n;
         p.K = 3 * dim;
         p.scale = 1.f;
-        p.residual_batch = nf;
-        p.residual_stride = 3 * dim;
+        p.identity = 1;
         for (int side = 0; side < 2; ++side) {
             const float* f = side ? feats_k : feats_q;
             p.set[side] = {operand(side ? proj_k : proj_q, dim, 3 * dim, true), operand(f, n, 3 * dim, false),
-                           hats + side * n_heads * nd, f};
+                           hats + side * n_heads * nd};
         }
         if (int rc = launch_gemm("veda_score_bias (projections)", p, expand, false, di, s)) return rc;
         train::Args l{};
@@ -336,7 +335,7 @@ extern "C" int veda_score_bias(const veda_layout* layout, const float* feats_q, 
         l.M = l.N = n;
         l.K = dim;
         l.scale = float(1.0 / std::sqrt(double(dim)));
-        l.set[0] = {operand(hats + n_heads * nd, n, dim, false), operand(hats, n, dim, false), scores, nullptr};
+        l.set[0] = {operand(hats + n_heads * nd, n, dim, false), operand(hats, n, dim, false), scores};
         l.one_span = layout->span_grid.size() == 4;
         if (bias) l.table = table;
         l.tile_num = reinterpret_cast<const int4*>(dc->tile_num);
@@ -503,9 +502,9 @@ extern "C" int veda_score_backward(const veda_layout* layout, const float* feats
         p.scale = 1.f;
         for (int side = 0; side < 2; ++side) {
             x.set[side] = {operand(hats + (side ? 0 : n_heads * nd), dim, n, true), operand(d_scores, n, n, side == 1),
-                           dx + side * n_heads * nd, nullptr};
+                           dx + side * n_heads * nd};
             p.set[side] = {operand(dx + side * n_heads * nd, dim, n, true), operand(side ? feats_k : feats_q, 3 * dim, n, true),
-                           side ? d_proj_k : d_proj_q, nullptr};
+                           side ? d_proj_k : d_proj_q};
         }
         if (int rc = launch_gemm("veda_score_backward (projected features)", x, BiasExpand{}, false, di, s)) return rc;
         return launch_gemm("veda_score_backward (projections)", p, BiasExpand{}, true, di, s);
