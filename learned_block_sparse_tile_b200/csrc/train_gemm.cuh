@@ -24,9 +24,11 @@
 //                stages of A's hi and lo parts (256-511)
 //   warp 2       TMA producer: raw slices of both operands into the split groups' stages
 //   warps 1, 3   the bias table that the score launch after this one reads, where it is asked for
-//   warps 4-11   epilogue, two warps per lane quarter with half of the columns each; their sums start from what is added
-//                to the product, whose loads pass while the tile is computed
-//   warps 12-23  split, three groups with a stage each that take the slices in turn, so that one group's waits pass while
+//   8 or 16      epilogue warps, two or four per lane quarter with a part of the columns each; their sums start from the bias,
+//                whose loads pass while the tile is computed. Scores, whose tiles have few slices for their 128 x 128
+//                biases and stores, take four warps a quarter (104k rows, 24 heads: 93 us; two: 96), gradients two (96 us;
+//                four: 102)
+//   12           split warps, three groups with a stage each that take the slices in turn, so that one group's waits pass while
 //                others work. Thread i of 128 has row i of both operands: it reads its 32 values of K (rows of K lie in
 //                the 128-byte swizzle, so that 8 lanes' 16-byte pieces fall into 8 different banks; columns are
 //                neighbours for neighbouring lanes), and writes A's parts to its TMEM lane and B's in the swizzle that
@@ -66,8 +68,6 @@ constexpr int kRawBytes = kPart + kRawB;  // A, B
 constexpr int kOffRaw = kStages * kStageBytes;
 constexpr int kOffBar = kOffRaw + kStages * kRawBytes;
 static_assert(kRawBytes % 1024 == 0, "raw slices lie in whole swizzle atoms");
-constexpr int kThreads = 768;
-constexpr int kEpilogue = 256;   // threads
 constexpr int kGroup = 128;      // threads of one split group; as many groups as stages
 constexpr uint32_t kStageA = 256;  // TMEM column of the first stage
 constexpr int kTimeoutBit = 1;
@@ -250,13 +250,17 @@ __device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_
         : "memory");
 }
 
-__global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Args a,
+// kParts: epilogue warps per lane quarter, and the parts of a tile's columns
+constexpr int threads_of(int parts) { return 32 * (4 + 4 * parts) + kStages * kGroup; }
+template <int kParts>
+__global__ void __launch_bounds__(threads_of(kParts), 1) gemm_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Args a,
                                                            const __grid_constant__ BiasExpand expand) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     Bars& B = *reinterpret_cast<Bars*>(smem + kOffBar);
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(&B + 1);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+    constexpr int kWide = kBN / kParts, kSplitWarp = 4 + 4 * kParts;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int nk = (a.K + kBK - 1) / kBK;
     const uint64_t tmo = a.timeout_ns;
@@ -272,7 +276,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
         }
         for (int s = 0; s < 2; ++s) {
             ptx::mbar_init(&B.acc_full[s], 1);
-            ptx::mbar_init(&B.acc_empty[s], kEpilogue);
+            ptx::mbar_init(&B.acc_empty[s], 128 * kParts);
         }
         ptx::mbar_init(&B.drain, 1);
         *abort_flag = 0;
@@ -287,7 +291,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
     asm volatile("griddepcontrol.wait;" ::: "memory");
 
     if (warp < 4) {
-        ptx::regs_dec<56>();
+        ptx::regs_dec<kParts == 2 ? 56 : 40>();
         if (warp == 0) {
             // ------------------------------------------------------------------------ MMA issuer
             constexpr uint32_t kId = tf32x3::idesc(kBM, kBN);
@@ -380,23 +384,24 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
             // ------------------------------------------------------------------------ the bias table (warps 1 and 3)
             for (int i = (blockIdx.x * 2 + (warp >> 1)) * 32 + lane; i < expand.count + 2; i += gridDim.x * 64) bias_expand(expand, i);
         }
-    } else if (warp < 12) {
+    } else if (warp < kSplitWarp) {
         // ---------------------------------------------------------------------------- epilogue
-        ptx::regs_inc<88>();
-        const int q = warp & 3, half = (warp - 4) >> 2;  // TMEM lane quarter (m 32 q ..), columns 64 half ..
+        if constexpr (kParts == 2) ptx::regs_inc<88>();
+        else ptx::regs_dec<56>();
+        const int q = warp & 3, part = (warp - 4) >> 2;  // TMEM lane quarter (m 32 q ..), columns kWide part ..
         int g = 0;
         bool stop = false;
         for (int t = blockIdx.x; t < a.n_tiles && !stop; t += gridDim.x) {
             const Tile w(a, t);
-            const uint32_t lanes = tmem + (uint32_t(32 * q) << 16) + uint32_t(64 * half);
-            const int m = w.m0 + 32 * q + lane, mm = min(m, a.M - 1), n0 = w.n0 + 64 * half;
+            const uint32_t lanes = tmem + (uint32_t(32 * q) << 16) + uint32_t(kWide * part);
+            const int m = w.m0 + 32 * q + lane, mm = min(m, a.M - 1), n0 = w.n0 + kWide * part;
             const int left = a.N - n0;
-            float acc[64];  // what is added to the product, over its scale, then the sums; loads from clamped places
+            float acc[kWide];  // what is added to the product, over its scale, then the sums; loads from clamped places
             if (a.table) {
                 const float* table = a.table + w.batch * a.table_stride;
                 const int4 key = a.tile_num[mm];
 #pragma unroll
-                for (int j = 0; j < 64; j += 32) {
+                for (int j = 0; j < kWide; j += 32) {
                     const int4 mine = a.tile_num[min(n0 + j + lane, a.N - 1)];
 #pragma unroll
                     for (int x = 0; x < 32; ++x) {
@@ -410,11 +415,11 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
                 }
             } else {
 #pragma unroll
-                for (int x = 0; x < 64; ++x) acc[x] = 0.f;
+                for (int x = 0; x < kWide; ++x) acc[x] = 0.f;
             }
             const auto add = [&](uint32_t from) {
 #pragma unroll
-                for (int j = 0; j < 64; j += 16) {
+                for (int j = 0; j < kWide; j += 16) {
                     uint32_t x[16];
                     ptx::tmem_ld16(from + j, x);
                     ptx::tmem_wait_ld();
@@ -437,20 +442,21 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
             if (m < a.M) {
                 // (a select, not a.set[w.set]: a runtime index into the kernel arguments would copy them to the stack)
                 float* C = (w.set ? a.set[1].C : a.set[0].C) + int64_t(w.batch) * a.M * a.N + int64_t(n0) * a.M + m;
-                if (left >= 64) {
+                if (left >= kWide) {
 #pragma unroll
-                    for (int x = 0; x < 64; ++x) C[uint32_t(x) * uint32_t(a.M)] = acc[x] * a.scale;
+                    for (int x = 0; x < kWide; ++x) C[uint32_t(x) * uint32_t(a.M)] = acc[x] * a.scale;
                 } else {
 #pragma unroll
-                    for (int x = 0; x < 64; ++x)
+                    for (int x = 0; x < kWide; ++x)
                         if (x < left) C[uint32_t(x) * uint32_t(a.M)] = acc[x] * a.scale;
                 }
             }
         }
     } else {
         // ---------------------------------------------------------------------------- split
-        ptx::regs_dec<80>();
-        const int s = (warp - 12) >> 2, i = threadIdx.x & (kGroup - 1);  // the group's number is its stage's
+        if constexpr (kParts == 2) ptx::regs_dec<80>();
+        else ptx::regs_inc<80>();
+        const int s = (warp - kSplitWarp) >> 2, i = threadIdx.x & (kGroup - 1);  // the group's number is its stage's
         const uint32_t stage_a = tmem + kStageA + uint32_t(64 * s) + (uint32_t(32 * (warp & 3)) << 16);
         uint8_t* stage_b = smem + s * kStageBytes;
         const uint8_t* raw = smem + kOffRaw + s * kRawBytes;

@@ -126,10 +126,11 @@ int operand_maps(CUtensorMap* m, const train::Operand& o, int K, int batches) {
 }
 
 // `after`: the launch before it on the stream is one of this call's, and its start may overlap that one's end
+template <int kParts>
 int launch_gemm(const char* what, train::Args a, const BiasExpand& expand, bool after, const DeviceInfo& di, cudaStream_t s) {
     static std::atomic<bool> set[kMaxDevices];
     if (!set[di.ordinal].load()) {
-        cudaError_t e = cudaFuncSetAttribute(train::gemm_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(train::kSmem));
+        cudaError_t e = cudaFuncSetAttribute(train::gemm_kernel<kParts>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(train::kSmem));
         if (e != cudaSuccess)
             return fail(VEDA_ERR_CUDA, std::string("cudaFuncSetAttribute(train gemm_kernel): ") + cudaGetErrorString(e));
         set[di.ordinal].store(true);
@@ -148,7 +149,7 @@ int launch_gemm(const char* what, train::Args a, const BiasExpand& expand, bool 
     }
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(unsigned(std::min(a.n_tiles, di.sms)));
-    cfg.blockDim = dim3(train::kThreads);
+    cfg.blockDim = dim3(train::threads_of(kParts));
     cfg.dynamicSmemBytes = train::kSmem;
     cfg.stream = s;
     cudaLaunchAttribute overlap{};
@@ -156,7 +157,7 @@ int launch_gemm(const char* what, train::Args a, const BiasExpand& expand, bool 
     overlap.val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = &overlap;
     cfg.numAttrs = after ? 1 : 0;
-    cudaError_t e = cudaLaunchKernelEx(&cfg, train::gemm_kernel, m, a, expand);
+    cudaError_t e = cudaLaunchKernelEx(&cfg, train::gemm_kernel<kParts>, m, a, expand);
     if (e != cudaSuccess) return fail(VEDA_ERR_CUDA, std::string(what) + ": " + cudaGetErrorString(e));
     return launch_status(what);
 }
@@ -328,7 +329,7 @@ extern "C" int veda_score_bias(const veda_layout* layout, const float* feats_q, 
             p.set[side] = {operand(side ? proj_k : proj_q, dim, 3 * dim, true), operand(f, n, 3 * dim, false),
                            hats + side * n_heads * nd};
         }
-        if (int rc = launch_gemm("veda_score_bias (projections)", p, expand, false, di, s)) return rc;
+        if (int rc = launch_gemm<4>("veda_score_bias (projections)", p, expand, false, di, s)) return rc;
         train::Args l{};
         l.n_sets = 1;
         l.nb = n_heads;
@@ -341,7 +342,7 @@ extern "C" int veda_score_bias(const veda_layout* layout, const float* feats_q, 
         l.tile_num = reinterpret_cast<const int4*>(dc->tile_num);
         l.table_stride = offsets + 2;
         l.offsets = offsets;
-        return launch_gemm("veda_score_bias (logits)", l, BiasExpand{}, true, di, s);
+        return launch_gemm<4>("veda_score_bias (logits)", l, BiasExpand{}, true, di, s);
     });
 }
 
@@ -506,7 +507,7 @@ extern "C" int veda_score_backward(const veda_layout* layout, const float* feats
             p.set[side] = {operand(dx + side * n_heads * nd, dim, n, true), operand(side ? feats_k : feats_q, 3 * dim, n, true),
                            side ? d_proj_k : d_proj_q};
         }
-        if (int rc = launch_gemm("veda_score_backward (projected features)", x, BiasExpand{}, false, di, s)) return rc;
-        return launch_gemm("veda_score_backward (projections)", p, BiasExpand{}, true, di, s);
+        if (int rc = launch_gemm<2>("veda_score_backward (projected features)", x, BiasExpand{}, false, di, s)) return rc;
+        return launch_gemm<2>("veda_score_backward (projections)", p, BiasExpand{}, true, di, s);
     });
 }
