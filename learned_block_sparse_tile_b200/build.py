@@ -11,7 +11,7 @@ LIB = os.path.join(HERE, "libveda.so")
 
 SOURCES = ["veda_api.cu", "veda_plan.cpp", "veda_score_noalloc.cu", "veda_train.cu"]
 HEADERS = ["veda_internal.h", "ptx.cuh", "gather.cuh", "score.cuh", "select.cuh", "attend.cuh", "attend_pair.cuh",
-           "quant.cuh", "bias.cuh", "distill.cuh", "train_gemm.cuh", "teacher.cuh", "tf32.cuh", "wait.cuh"]
+           "quant.cuh", "bias.cuh", "distill.cuh", "train_gemm.cuh", "teacher.cuh", "tf32.cuh", "wait.cuh", "warp.cuh"]
 
 
 def nvcc_path():

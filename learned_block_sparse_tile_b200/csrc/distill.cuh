@@ -22,6 +22,7 @@
 #include <cstdint>
 
 #include "ptx.cuh"
+#include "warp.cuh"
 
 namespace veda {
 
@@ -42,11 +43,10 @@ struct DistillArgs {
     int* err;
 };
 
-// One value for the row's kWarps warps. `scratch` holds kWarps floats, free again for the next reduction but one.
+// One value for the row's kWarps warps, from one per warp. `scratch` holds kWarps floats, free again for the next reduction
+// but one.
 template <int kWarps, class Op>
-__device__ __forceinline__ float row_reduce(float v, float* scratch, Op op) {
-#pragma unroll
-    for (int o = 16; o; o >>= 1) v = op(v, __shfl_xor_sync(0xffffffffu, v, o));
+__device__ __forceinline__ float across_warps(float v, float* scratch, Op op) {
     if constexpr (kWarps > 1) {
         if ((threadIdx.x & 31) == 0) scratch[threadIdx.x >> 5] = v;
         __syncthreads();
@@ -55,6 +55,16 @@ __device__ __forceinline__ float row_reduce(float v, float* scratch, Op op) {
         for (int w = 1; w < kWarps; ++w) v = op(v, scratch[w]);
     }
     return v;
+}
+template <int kWarps>
+__device__ __forceinline__ float row_max(float v, float* scratch) {
+    return across_warps<kWarps>(warp_max(v), scratch, [](float x, float y) { return fmaxf(x, y); });
+}
+template <int kWarps>
+__device__ __forceinline__ float row_sum(float v, float* scratch) {
+#pragma unroll
+    for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return across_warps<kWarps>(v, scratch, [](float x, float y) { return x + y; });
 }
 
 // Rows of up to 32 * kPer * kWarps columns. One warp per row: four rows in a CTA; else one row in a CTA. The registers are
@@ -70,8 +80,6 @@ __global__ void __launch_bounds__(kWarps == 1 ? 128 : 32 * kWarps, kWarps == 1 ?
     const float* s = a.scores + r * a.n;
     const int32_t* idx = a.t_idx + r * a.width;
     const float* val = a.t_val + r * (a.by_column ? a.n : a.width);
-    const auto maxf = [](float x, float y) { return fmaxf(x, y); };
-    const auto add = [](float x, float y) { return x + y; };
 
     const int given = a.t_cnt[r];
     float v[kPer];
@@ -128,8 +136,8 @@ __global__ void __launch_bounds__(kWarps == 1 ? 128 : 32 * kWarps, kWarps == 1 ?
     float ms = -INFINITY;
 #pragma unroll
     for (int k = 0; k < kPer; ++k) ms = fmaxf(ms, v[k]);
-    ms = row_reduce<kWarps>(ms, scratch[0], maxf);
-    mt = row_reduce<kWarps>(mt, scratch[1], maxf);
+    ms = row_max<kWarps>(ms, scratch[0]);
+    mt = row_max<kWarps>(mt, scratch[1]);
 
     const float c2 = a.inv_tau * 1.4426950408889634f;
     float zs = 0.f;
@@ -151,10 +159,10 @@ __global__ void __launch_bounds__(kWarps == 1 ? 128 : 32 * kWarps, kWarps == 1 ?
 #pragma unroll
     for (int u = 0; u < kListed; ++u) t[u] = entry(t[u], x[u]);
     for (int e = lane + kLanes * kListed; e < cnt; e += kLanes) entry(val[a.by_column ? idx[e] : e], __ldg(s + idx[e]));
-    zs = row_reduce<kWarps>(zs, scratch[0], add);
-    zt = row_reduce<kWarps>(zt, scratch[1], add);
+    zs = row_sum<kWarps>(zs, scratch[0]);
+    zt = row_sum<kWarps>(zt, scratch[1]);
     if constexpr (kWarps > 1) __syncthreads();
-    gap = row_reduce<kWarps>(gap, scratch[0], add);
+    gap = row_sum<kWarps>(gap, scratch[0]);
     // no target (an empty list, or only -inf in it) or no student column above -inf: the row is left out
     const bool out = zt == 0.f || zs == 0.f;
     const float w = a.row_weight ? a.row_weight[r] : 1.f;

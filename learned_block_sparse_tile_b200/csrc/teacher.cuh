@@ -25,6 +25,7 @@
 
 #include "ptx.cuh"
 #include "wait.cuh"
+#include "warp.cuh"
 
 namespace veda {
 namespace teacher {
@@ -84,13 +85,6 @@ struct Unit {
         p1 = int(int64_t(a.pairs) * (run + 1) / a.runs);
     }
 };
-
-// the largest value of the warp (a warp-wide reduction instruction of this architecture)
-__device__ __forceinline__ float warp_max(float v) {
-    float r;
-    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
-    return r;
-}
 
 // best = max(best, the first `cols` of 32 columns)
 __device__ __forceinline__ float take(float best, const uint32_t (&v)[32], int cols) {

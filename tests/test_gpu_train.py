@@ -374,6 +374,72 @@ def test_score_backward(geo, dim, heads):
         within(out, ft @ dx, ft.abs() @ tx + product_tol(ft, dx.abs() + tx, n))
 
 
+# ---------------------------------------------------------------------------------------- limits of the sizes
+
+
+def test_many_heads():
+    # more heads than SMs, and than the bias gradient has chunks for
+    geo, H, D, reach, far = Geometry([((2, 16, 24), (2, 8, 8))], text=130), 301, 64, (3, 2, 3), (8, 8, 8)
+    n = geo.n
+    q, k = T.tile_rows(geo, 1, H, D), T.tile_rows(geo, 3, H, D)
+    within(teacher(geo, q, k), T.plain_teacher(geo, q, k), teacher_tol(q, k, None))
+    fq, fk, pq, pk = feats(1, H, n, D), feats(4, H, n, D), projections(7, H, D), projections(8, H, D)
+    bias = randn(9, H, L.veda_bias_buckets(reach, far))
+    out, hats = score_bias(geo, fq, fk, pq, pk, reach, far, bias)
+    qh, kh = T.plain_hats(fq, fk, pq, pk)
+    index = torch.as_tensor(L.veda_bias_index(geo.layout, reach, far), device=DEV).long()
+    want = qh @ kh.transpose(1, 2) / math.sqrt(D) + bias.double()[:, index]
+    # 3 D and D additions, each at most 2^-23 of sums of magnitudes below 2^9
+    within(out, want, torch.full_like(want, 4 * D * 2 * EPS * 2.0 ** 9))
+    scores = randn(11, H, n, n)
+    idx, val, cnt = T.top_lists(geo, randn(12, H, n, n), 3)
+    loss, d = distill(geo, scores, idx, val, cnt, 2.0)
+    check_distill(geo, scores, idx, val, cnt, 2.0, None, loss, d)
+    sums = torch.zeros(H, bias.shape[1], dtype=torch.float64, device=DEV)
+    sums.index_add_(1, index.reshape(-1), d.double().reshape(H, -1))
+    within(bias_backward(geo, d, reach, far), sums, torch.full_like(sums, (3 * n + 64) * EPS * n * n))
+    got = score_backward(geo, fq, fk, hats, d)
+    again = score_backward(geo, fq, fk, hats, d)
+    assert all(torch.equal(a, b) and bool(torch.isfinite(a).all()) for a, b in zip(got, again))
+
+
+def test_largest_layout():
+    # 16,384 tiles of one row each: every operator at the limit, compared on some rows
+    geo, D, reach, far = Geometry([((16384, 1, 1), (1, 1, 128))]), 64, (8, 1, 1), (4000, 2, 2)
+    n, some = geo.n, torch.tensor([0, 1, 127, 128, 8191, 12345, 16383], device=DEV)
+    q, k = T.tile_rows(geo, 1, 1, D), T.tile_rows(geo, 3, 1, D)
+    rows, keys = (x[0].reshape(n, 128, D)[:, 0].double() for x in (q, k))
+    out = teacher(geo, q, k)
+    within(out[0, some], rows[some] @ keys.T / 8, teacher_tol(q, k, None))
+    del out
+    fq, fk, pq, pk = feats(1, 1, n, D), feats(4, 1, n, D), projections(7, 1, D), projections(8, 1, D)
+    bias = randn(9, 1, L.veda_bias_buckets(reach, far))
+    scores, hats = score_bias(geo, fq, fk, pq, pk, reach, far, bias)
+    qh, kh = T.plain_hats(fq, fk, pq, pk)
+    r = torch.arange(n, device=DEV)[None] - some[:, None]
+    classes = torch.as_tensor(L.veda_bias_index(Geometry([((300, 1, 1), (1, 1, 128))]).layout, (8, 1, 1), (4000, 2, 2))[0], device=DEV)
+    near = (r.abs() < 300)
+    index = torch.where(r > 0, classes[r.clamp(0, 299)].long(), torch.zeros_like(r))
+    want = qh[0, some] @ kh[0].T / 8
+    got = scores[0, some].double() - want
+    # offsets of 0 to 299 keys behind have the buckets of a short line; differences stay within the scores' error
+    ahead = near & (r >= 0)
+    tol = 4 * D * 2 * EPS * 2.0 ** 9
+    assert float((got - bias[0].double()[index])[ahead].abs().max()) <= tol
+    del scores
+    ds = randn(11, 1, n, n)
+    dq, dk = score_backward(geo, fq, fk, hats, ds)
+    dx = ds[0].double() @ hats[1, 0].double() / 8
+    want = fq[0].double().T @ dx
+    bound = fq[0].abs().double().T @ product_tol(ds[0].double(), hats[1, 0].double() / 8, n)
+    within(dq[0], want, bound + product_tol(fq[0].double().T, dx, n))
+    total = bias_backward(geo, ds, reach, far)
+    assert abs(float(total.double().sum()) - float(ds.double().sum())) <= (3 * n + 64) * EPS * float(ds.abs().double().sum())
+    zero = float(torch.diagonal(ds[0]).double().sum())  # distance 0 is a bucket of its own
+    at = int(L.veda_bias_index(Geometry([((1, 1, 1), (1, 1, 128))]).layout, reach, far)[0, 0])
+    assert abs(float(total[0, at]) - zero) <= (3 * n + 64) * EPS * float(torch.diagonal(ds[0]).abs().double().sum())
+
+
 # ------------------------------------------------------------------------------------------------ together
 
 
