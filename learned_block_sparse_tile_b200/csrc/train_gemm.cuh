@@ -19,7 +19,8 @@
 // so that A's rows are innermost in memory (a warp reads 32 neighbouring rows at one k), which also makes the
 // lanes of an accumulator neighbours in C: the epilogue stores whole 128-byte lines without a transpose.
 //
-// Persistent CTAs walk 128 x 128 tiles; K runs in slices of 32:
+// Persistent CTAs walk 128 x 128 tiles; the tiles that do not fill the last round of CTAs are cut along K where that saves
+// more slices than joining them costs (join_kernel). K runs in slices of 32:
 //   warp 0       MMA issuer, 12 MMAs per slice; warp 1 owns the TMEM: the sums twice (columns 0-255) and kStages
 //                stages of A's hi and lo parts (256-511)
 //   warp 2       TMA producer: raw slices of both operands into the split groups' stages
@@ -112,7 +113,9 @@ struct Args {
     Set set[2];
     int n_sets, nb;         // operand sets (1 or 2) of one shape, batches in each
     int M, N, K;
-    int tiles_m, tiles_n, n_tiles;
+    int tiles_m, tiles_n;
+    int full, parts, n_units;  // tiles of one unit each, then the others' K in `parts` units each
+    float* partial;            // [units of split tiles][128 of N][128 of M]
     float scale;
     int identity;           // A(m, m) + 1 in the place of A(m, m)
     // the bias of score tiles (table null: none), m the key and n the query: scale table[batch][key number + query number]
@@ -135,6 +138,48 @@ struct Tile {
         n0 = (r % a.tiles_n) * kBN;
     }
 };
+
+// A work unit: slices [k0, k1) of a tile; the tiles that do not fill the last round of CTAs are cut along K.
+struct Unit : Tile {
+    int k0 = 0, k1, part = -1;  // part: the unit's place among those of split tiles, or -1
+    __device__ __forceinline__ Unit(const Args& a, int u, int nk) : Tile(a, u), k1(nk) {
+        if (u >= a.full) {
+            part = u - a.full;
+            const int t = part / a.parts, p = part - t * a.parts;
+            static_cast<Tile&>(*this) = Tile(a, a.full + t);
+            k0 = nk * p / a.parts;
+            k1 = nk * (p + 1) / a.parts;
+        }
+    }
+};
+__device__ __forceinline__ int unit_slices(const Args& a, int u, int nk) {
+    if (u < a.full) return nk;
+    const int p = (u - a.full) % a.parts;
+    return nk * (p + 1) / a.parts - nk * p / a.parts;
+}
+
+// C of the split tiles: their parts' sums, in order (a programmatic dependent launch; 16 CTAs a tile)
+__global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ Args a) {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const Tile w(a, a.full + blockIdx.y);
+    const float* p = a.partial + int64_t(blockIdx.y) * a.parts * (kBM * kBN);
+    float* C = (w.set ? a.set[1].C : a.set[0].C) + int64_t(w.batch) * a.M * a.N;
+    const int e = (blockIdx.x * 256 + threadIdx.x) * 4, n = w.n0 + e / kBM, m = w.m0 + e % kBM;
+    float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int x = 0; x < a.parts; ++x) {
+        const float4 v = *reinterpret_cast<const float4*>(p + int64_t(x) * (kBM * kBN) + e);
+        sum.x += v.x;
+        sum.y += v.y;
+        sum.z += v.z;
+        sum.w += v.w;
+    }
+    const float v[4] = {sum.x, sum.y, sum.z, sum.w};
+    if (n < a.N)
+        for (int x = 0; x < 4; ++x)
+            if (m + x < a.M) C[int64_t(n) * a.M + m + x] = v[x] * a.scale;
+}
 
 // Loads that stay where they are written, ahead of the waits that hide their latency.
 __device__ __forceinline__ float load1(const float* p) {
@@ -297,8 +342,8 @@ __global__ void __launch_bounds__(threads_of(kParts), 1) gemm_kernel(const __gri
             constexpr uint32_t kId = tf32x3::idesc(kBM, kBN);
             int g = 0;  // slices consumed
             bool stop = false;
-            for (int t = blockIdx.x; t < a.n_tiles && !stop; t += gridDim.x) {
-                for (int kk = 0; kk < nk; ++kk, ++g) {
+            for (int u = blockIdx.x; u < a.n_units && !stop; u += gridDim.x) {
+                for (int left = unit_slices(a, u, nk); left > 0; --left, ++g) {
                     const int s = g % kStages, b = g & 1;
                     if (!warp_wait(&B.acc_empty[b], ((g >> 1) & 1) ^ 1, abort_flag, tmo) ||
                         !warp_wait(&B.full[s], (g / kStages) & 1, abort_flag, tmo)) {
@@ -331,18 +376,18 @@ __global__ void __launch_bounds__(threads_of(kParts), 1) gemm_kernel(const __gri
             const uint64_t keep = ptx::policy_evict_last();  // operand rows are read by several tiles
             int g = 0;
             bool stop = false;
-            for (int t = blockIdx.x; t < a.n_tiles && !stop; t += gridDim.x) {
-                const Tile w(a, t);
+            for (int u = blockIdx.x; u < a.n_units && !stop; u += gridDim.x) {
+                const Unit w(a, u, nk);
                 const int la = w.set ? a.set[1].a.layout : a.set[0].a.layout;
                 const int lb = w.set ? a.set[1].b.layout : a.set[0].b.layout;
                 const int dense = w.set ? a.set[1].b.dense : a.set[0].b.dense;
                 const int row0 = w.batch * (lb == kCols ? a.K : a.N);  // the batch's first row, over all of them
                 const CUtensorMap *ma = w.set ? &maps.a[1] : &maps.a[0], *mb = w.set ? maps.b[1] : maps.b[0];
-                for (int kk = 0; kk < nk; ++kk, ++g) {
+                for (int kk = w.k0; kk < w.k1; ++kk, ++g) {
                     const int s = g % kStages, ph = g / kStages, k0 = kk * kBK;
                     // a stage is refilled as soon as it is read, which leaves no time for memory's latency: the slice
                     // after the stages' comes into L2 meanwhile
-                    if (kk + kStages < nk && ptx::elect_one()) {
+                    if (kk + kStages < w.k1 && ptx::elect_one()) {
                         const int k1 = k0 + kStages * kBK;
                         prefetch_3d(ma, la == kCols ? w.m0 : k1, la == kCols ? k1 : w.m0, w.batch);
                         if (dense) {
@@ -391,8 +436,8 @@ __global__ void __launch_bounds__(threads_of(kParts), 1) gemm_kernel(const __gri
         const int q = warp & 3, part = (warp - 4) >> 2;  // TMEM lane quarter (m 32 q ..), columns kWide part ..
         int g = 0;
         bool stop = false;
-        for (int t = blockIdx.x; t < a.n_tiles && !stop; t += gridDim.x) {
-            const Tile w(a, t);
+        for (int u = blockIdx.x; u < a.n_units && !stop; u += gridDim.x) {
+            const Unit w(a, u, nk);
             const uint32_t lanes = tmem + (uint32_t(32 * q) << 16) + uint32_t(kWide * part);
             const int m = w.m0 + 32 * q + lane, mm = min(m, a.M - 1), n0 = w.n0 + kWide * part;
             const int left = a.N - n0;
@@ -427,7 +472,7 @@ __global__ void __launch_bounds__(threads_of(kParts), 1) gemm_kernel(const __gri
                     for (int e = 0; e < 16; ++e) acc[j + e] += __uint_as_float(x[e]);
                 }
             };
-            for (int kk = 0; kk < nk; ++kk, ++g) {
+            for (int kk = w.k0; kk < w.k1; ++kk, ++g) {
                 const int b = g & 1;
                 if (!warp_wait(&B.acc_full[b], (g >> 1) & 1, abort_flag, tmo)) {
                     stop = true;
@@ -439,7 +484,11 @@ __global__ void __launch_bounds__(threads_of(kParts), 1) gemm_kernel(const __gri
                 ptx::mbar_arrive(&B.acc_empty[b]);
             }
             if (stop) break;
-            if (m < a.M) {
+            if (w.part >= 0) {
+                float* P = a.partial + (int64_t(w.part) * kBN + kWide * part) * kBM + (m - w.m0);
+#pragma unroll
+                for (int x = 0; x < kWide; ++x) P[x * kBM] = acc[x];
+            } else if (m < a.M) {
                 // (a select, not a.set[w.set]: a runtime index into the kernel arguments would copy them to the stack)
                 float* C = (w.set ? a.set[1].C : a.set[0].C) + int64_t(w.batch) * a.M * a.N + int64_t(n0) * a.M + m;
                 if (left >= kWide) {
@@ -460,21 +509,26 @@ __global__ void __launch_bounds__(threads_of(kParts), 1) gemm_kernel(const __gri
         const uint32_t stage_a = tmem + kStageA + uint32_t(64 * s) + (uint32_t(32 * (warp & 3)) << 16);
         uint8_t* stage_b = smem + s * kStageBytes;
         const uint8_t* raw = smem + kOffRaw + s * kRawBytes;
-        // this group's slices, every kStages-th of the CTA's sequence: tile t, slice kk, number `use` of the group
-        int t = blockIdx.x, kk = s, use = 0;
-        while (kk >= nk && t < a.n_tiles) {
-            kk -= nk;
-            t += gridDim.x;
-        }
-        Tile w(a, t);
-        while (t < a.n_tiles) {
-            const Operand& ob = w.set ? a.set[1].b : a.set[0].b;
-            const int la = w.set ? a.set[1].a.layout : a.set[0].a.layout;
-            int next = t, next_kk = kk + kStages;
-            while (next_kk >= nk && next < a.n_tiles) {
-                next_kk -= nk;
-                next += gridDim.x;
+        // this group's slices, every kStages-th of the CTA's sequence: unit u, its slice `at`, number `use` of the group
+        int u = blockIdx.x, at = s, use = 0;
+        int slices = u < a.n_units ? unit_slices(a, u, nk) : 0;
+        const auto settle = [&] {  // `at` within its unit
+            while (u < a.n_units && at >= slices) {
+                at -= slices;
+                u += gridDim.x;
+                if (u < a.n_units) slices = unit_slices(a, u, nk);
             }
+        };
+        settle();
+        int mine = -1;
+        Unit w(a, min(u, a.n_units - 1), nk);
+        while (u < a.n_units) {
+            if (u != mine) {
+                w = Unit(a, u, nk);
+                mine = u;
+            }
+            const Operand& ob = w.set ? a.set[1].b : a.set[0].b;
+            const int la = w.set ? a.set[1].a.layout : a.set[0].a.layout, kk = w.k0 + at;
             if (!warp_wait(&B.raw_full[s], use & 1, abort_flag, tmo) ||
                 !warp_wait(&B.empty[s], (use & 1) ^ 1, abort_flag, tmo))
                 break;
@@ -513,9 +567,8 @@ __global__ void __launch_bounds__(threads_of(kParts), 1) gemm_kernel(const __gri
             ptx::tc_fence_before();
             __syncwarp();
             if (lane == 0) ptx::mbar_arrive(&B.full[s]);
-            if (next != t) w = Tile(a, next);
-            t = next;
-            kk = next_kk;
+            at += kStages;
+            settle();
             ++use;
         }
     }

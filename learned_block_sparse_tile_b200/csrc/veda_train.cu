@@ -125,6 +125,9 @@ int operand_maps(CUtensorMap* m, const train::Operand& o, int K, int batches) {
     return VEDA_OK;
 }
 
+constexpr int kSplitUnits = 148, kSplitSlices = 4, kJoinSlices = 6;
+constexpr size_t kSplitBytes = size_t(kSplitUnits) * train::kBM * train::kBN * sizeof(float);  // parts of split tiles
+
 // `after`: the launch before it on the stream is one of this call's, and its start may overlap that one's end
 template <int kParts>
 int launch_gemm(const char* what, train::Args a, const BiasExpand& expand, bool after, const DeviceInfo& di, cudaStream_t s) {
@@ -138,8 +141,15 @@ int launch_gemm(const char* what, train::Args a, const BiasExpand& expand, bool 
     a.tiles_m = (a.M + train::kBM - 1) / train::kBM;
     a.tiles_n = (a.N + train::kBN - 1) / train::kBN;
     const int64_t tiles = int64_t(a.n_sets) * a.nb * a.tiles_m * a.tiles_n;
-    if (tiles > INT32_MAX) return fail(VEDA_ERR_UNSUPPORTED, std::string(what) + ": too many tiles for one launch");
-    a.n_tiles = int(tiles);
+    if (tiles > INT32_MAX - kSplitUnits) return fail(VEDA_ERR_UNSUPPORTED, std::string(what) + ": too many tiles for one launch");
+    // Tiles past whole rounds of CTAs are cut along K into as many parts as CTAs are left, of at least kSplitSlices slices,
+    // when that shortens the last round by more than joining the parts takes (about kJoinSlices slices' time). 819 tiles,
+    // D 128, both gradients: 24 heads 96 -> 93 us, 8 heads 50 -> 46, 1 head 46 -> 24.
+    const int nk = (a.K + train::kBK - 1) / train::kBK, rest = int(tiles % di.sms);
+    a.parts = rest && a.partial ? std::min(std::min(di.sms, kSplitUnits) / rest, nk / kSplitSlices) : 1;
+    if (a.parts < 2 || nk - (nk + a.parts - 1) / a.parts < kJoinSlices) a.parts = 1;
+    a.full = int(tiles) - (a.parts > 1 ? rest : 0);
+    a.n_units = a.full + (a.parts > 1 ? rest * a.parts : 0);
     a.timeout_ns = wait_timeout_ns();
     a.err = di.err;
     train::Maps m{};
@@ -148,7 +158,7 @@ int launch_gemm(const char* what, train::Args a, const BiasExpand& expand, bool 
         if (int rc = operand_maps(m.b[i], a.set[i].b, a.K, a.nb)) return rc;
     }
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(unsigned(std::min(a.n_tiles, di.sms)));
+    cfg.gridDim = dim3(unsigned(std::min(a.n_units, di.sms)));
     cfg.blockDim = dim3(train::threads_of(kParts));
     cfg.dynamicSmemBytes = train::kSmem;
     cfg.stream = s;
@@ -159,6 +169,14 @@ int launch_gemm(const char* what, train::Args a, const BiasExpand& expand, bool 
     cfg.numAttrs = after ? 1 : 0;
     cudaError_t e = cudaLaunchKernelEx(&cfg, train::gemm_kernel<kParts>, m, a, expand);
     if (e != cudaSuccess) return fail(VEDA_ERR_CUDA, std::string(what) + ": " + cudaGetErrorString(e));
+    if (int rc = launch_status(what)) return rc;
+    if (a.parts == 1) return VEDA_OK;
+    cfg.gridDim = dim3(train::kBM * train::kBN / 1024, unsigned(rest));
+    cfg.blockDim = dim3(256);
+    cfg.dynamicSmemBytes = 0;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, train::join_kernel, a);
+    if (e != cudaSuccess) return fail(VEDA_ERR_CUDA, std::string(what) + " (join): " + cudaGetErrorString(e));
     return launch_status(what);
 }
 
@@ -281,7 +299,7 @@ extern "C" int veda_teacher(const veda_layout* layout, const void* q_t, const vo
 
 extern "C" size_t veda_score_bias_workspace_bytes(const veda_layout* layout, int32_t n_heads, int32_t dim) {
     if (!layout || n_heads <= 0 || dim <= 0) return 0;
-    return round256(size_t(n_heads) * size_t(layout->bias_offsets + 2) * sizeof(float));
+    return kSplitBytes + round256(size_t(n_heads) * size_t(layout->bias_offsets + 2) * sizeof(float));
 }
 
 extern "C" int veda_score_bias(const veda_layout* layout, const float* feats_q, const float* feats_k, int32_t n_heads,
@@ -309,7 +327,7 @@ extern "C" int veda_score_bias(const veda_layout* layout, const float* feats_q, 
         const int n = layout->desc.n_video;
         const int offsets = layout->bias_offsets;
         cudaStream_t s = static_cast<cudaStream_t>(stream);
-        float* table = static_cast<float*>(workspace);
+        float* table = static_cast<float*>(workspace) + kSplitBytes / sizeof(float);  // behind the parts of split tiles
         BiasExpand expand{};
         if (bias)
             expand = {bias, table, float(std::sqrt(double(dim))), reinterpret_cast<const int4*>(dc->span_grid),
@@ -324,6 +342,7 @@ extern "C" int veda_score_bias(const veda_layout* layout, const float* feats_q, 
         p.K = 3 * dim;
         p.scale = 1.f;
         p.identity = 1;
+        p.partial = static_cast<float*>(workspace);
         for (int side = 0; side < 2; ++side) {
             const float* f = side ? feats_k : feats_q;
             p.set[side] = {operand(side ? proj_k : proj_q, dim, 3 * dim, true), operand(f, n, 3 * dim, false),
@@ -467,7 +486,7 @@ extern "C" int veda_distill(const veda_layout* layout, const float* scores, int3
 
 extern "C" size_t veda_score_backward_workspace_bytes(const veda_layout* layout, int32_t n_heads, int32_t dim) {
     if (!layout || n_heads <= 0 || dim <= 0) return 0;
-    return round256(2 * size_t(n_heads) * size_t(layout->desc.n_video) * size_t(dim) * sizeof(float));
+    return kSplitBytes + round256(2 * size_t(n_heads) * size_t(layout->desc.n_video) * size_t(dim) * sizeof(float));
 }
 
 extern "C" int veda_score_backward(const veda_layout* layout, const float* feats_q, const float* feats_k, int32_t n_heads,
@@ -488,7 +507,7 @@ extern "C" int veda_score_backward(const veda_layout* layout, const float* feats
         if (int rc = current_device(&di)) return rc;
         const int n = layout->desc.n_video;
         const int64_t nd = int64_t(n) * dim;
-        float* dx = static_cast<float*>(workspace);
+        float* dx = static_cast<float*>(workspace) + kSplitBytes / sizeof(float);  // behind the parts of split tiles
         cudaStream_t s = static_cast<cudaStream_t>(stream);
         const float c = float(1.0 / std::sqrt(double(dim)));
         // dq_hat[i][d] = c sum_j dS[i][j] k_hat[j][d] and dk_hat[j][d] = c sum_i dS[i][j] q_hat[i][d], then
@@ -501,6 +520,7 @@ extern "C" int veda_score_backward(const veda_layout* layout, const float* feats
         p.N = 3 * dim;
         x.scale = c;
         p.scale = 1.f;
+        x.partial = p.partial = static_cast<float*>(workspace);
         for (int side = 0; side < 2; ++side) {
             x.set[side] = {operand(hats + (side ? 0 : n_heads * nd), dim, n, true), operand(d_scores, n, n, side == 1),
                            dx + side * n_heads * nd};

@@ -360,8 +360,19 @@ def score_backward(geo, fq, fk, hats, ds, **kw):
     return out
 
 
+@pytest.mark.parametrize("spans,dim,heads", [([((13, 48, 84), (1, 8, 16))], 128, 1), ([((13, 48, 84), (1, 8, 16))], 64, 5),
+                                             ([((26, 48, 84), (2, 16, 4))], 128, 2)])
+def test_score_backward_cut_along_k(spans, dim, heads):
+    # 468 and 819 tiles of few heads: the products' K is cut over the CTAs and joined
+    check_score_backward(Geometry(spans), dim, heads)
+
+
 @pytest.mark.parametrize("dim,heads", [(64, 3), (128, 1), (128, 2)])
 def test_score_backward(geo, dim, heads):
+    check_score_backward(geo, dim, heads)
+
+
+def check_score_backward(geo, dim, heads):
     n = geo.n
     fq, fk, hats = feats(1, heads, n, dim), feats(4, heads, n, dim), randn(7, 2, heads, n, dim)
     ds = torch.softmax(2 * randn(9, heads, n, n), 2) - torch.softmax(4 * randn(10, heads, n, n), 2)
