@@ -118,24 +118,24 @@ __device__ __forceinline__ void bias_interval(const int* starts, int reach, int 
 
 // Sums of one chunk of query rows, by offset first. Within a row no two keys of the query's span have the same offset, so
 // a row adds to as many different sums as it has columns: the CTA keeps one sum per offset in shared memory (fewer than 8
-// per tile), its threads add a row's columns without collisions, and a barrier parts the rows. Up to 1024 tiles there are
-// two sets of sums, for even and odd rows, and a barrier parts pairs of rows. Nothing
-// is atomic, and every sum is added up in row order. The loads run kDepth rows ahead in registers, because the rows' own
-// work is short: an addition in shared memory and a barrier; a warp waits for its newer loads with its older ones, so
-// they cover the latency of L2 and not of memory, and one thread asks for the chunk's next rows, a run of memory, in L2 further
-// ahead (104k rows, 24 heads, from HBM: 44 -> 32 us; from L2 24). At the end each bucket is the sum of a box of offsets. Bound by the chain of shared-memory addition and barrier,
-// with two CTAs on an SM taking turns; the floor is reading d_scores once.
+// per tile), its threads add a row's columns without collisions, and a barrier parts the rows. Nothing is atomic, and
+// every sum is added up in row order. The loads run kDepth rows ahead in registers, because the rows' own work is short:
+// an addition in shared memory and a barrier; a warp waits for its newer loads with its older ones, so they cover the
+// latency of L2 and not of memory, and one thread asks for the chunk's next rows, a run of memory, in L2 further ahead
+// (104k rows, 24 heads, from HBM: 44 -> 32 us). At the end each bucket is the sum of a box of offsets. Bound by the chain
+// of shared-memory addition and barrier, with up to three CTAs on an SM taking turns (104k, 24 heads: 28 us from HBM, 23
+// from L2; two CTAs: 32 and 24; two sets of sums and a barrier for each two rows gain nothing: 29 and 23); the floor is
+// reading d_scores once.
 template <int kPer, bool kOneSpan>
 __global__ void __launch_bounds__(512, kPer <= 4 ? 2 : 1) bias_backward_kernel(const BiasBackwardArgs a) {
     constexpr int kDepth = kPer <= 2 ? 8 : kPer <= 4 ? 4 : 2;
-    constexpr int kSets = kPer <= 2 ? 2 : 1;  // row i adds to set i % kSets
-    constexpr int kAhead = kDepth;            // rows asked for in L2 ahead of the loads
+    constexpr int kAhead = kDepth;  // rows asked for in L2 ahead of the loads
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    extern __shared__ float sums[];  // [kSets][offsets], 2 x 16 cross-span sums of the warps, then the rows' queries
+    extern __shared__ float sums[];  // [offsets], 2 x 16 cross-span sums of the warps, then the rows' queries
     const int head = blockIdx.y, pairs = a.b.buckets - 2, nt = blockDim.x;
     const int i0 = blockIdx.x * a.rows_per_chunk, i1 = min(a.n, i0 + a.rows_per_chunk);
-    int2* query = reinterpret_cast<int2*>(sums + (kSets * a.offsets + 32 + 1) / 2 * 2);  // {span, number}
-    const float* next = a.d_scores + (int64_t(head) * a.n + i0) * a.n + threadIdx.x;     // of the next row to load
+    int2* query = reinterpret_cast<int2*>(sums + (a.offsets + 32 + 1) / 2 * 2);      // {span, number}
+    const float* next = a.d_scores + (int64_t(head) * a.n + i0) * a.n + threadIdx.x;  // of the next row to load
     // rows [i, i + count) of the chunk into L2, in whole 16-byte parts
     const auto prefetch = [&](int i, int count) {
         const int rows = min(count, i1 - i);
@@ -168,7 +168,7 @@ __global__ void __launch_bounds__(512, kPer <= 4 ? 2 : 1) bias_backward_kernel(c
         const int4 q = a.tile_num[i];
         query[i - i0] = make_int2(q.x, q.z);
     }
-    for (int o = threadIdx.x; o < kSets * a.offsets; o += nt) sums[o] = 0.f;
+    for (int o = threadIdx.x; o < a.offsets; o += nt) sums[o] = 0.f;
     __syncthreads();
     float before = 0.f, behind = 0.f;
     for (int i = i0; i < i1; i += kDepth) {
@@ -177,7 +177,7 @@ __global__ void __launch_bounds__(512, kPer <= 4 ? 2 : 1) bias_backward_kernel(c
         for (int r = 0; r < kDepth; ++r) {
             if (i + r < i1) {
                 const int2 q = query[i - i0 + r];
-                float* at = sums + (r % kSets) * a.offsets + q.y;
+                float* at = sums + q.y;
 #pragma unroll
                 for (int k = 0; k < kPer; ++k) {
                     if (kOneSpan ? span[k] >= 0 : span[k] == q.x) {
@@ -189,10 +189,10 @@ __global__ void __launch_bounds__(512, kPer <= 4 ? 2 : 1) bias_backward_kernel(c
                 }
                 if (i + r + kDepth < i1) load(v[r]);
             }
-            if (r % kSets == kSets - 1) __syncthreads();
+            __syncthreads();
         }
     }
-    float* cross = sums + kSets * a.offsets;
+    float* cross = sums + a.offsets;
 #pragma unroll
     for (int o = 16; o; o >>= 1) {
         before += __shfl_xor_sync(0xffffffffu, before, o);
@@ -221,10 +221,7 @@ __global__ void __launch_bounds__(512, kPer <= 4 ? 2 : 1) bias_backward_kernel(c
                 for (int h = h0; h < h1; ++h)
                     for (int w = w0; w < w1; ++w)
 #pragma unroll 4
-                        for (int t = t0; t < t1; ++t) {
-                            const float* x = at + (h * rw + w) * rt + t;
-                            sum += kSets == 2 ? x[0] + x[a.offsets] : x[0];
-                        }
+                        for (int t = t0; t < t1; ++t) sum += at[(h * rw + w) * rt + t];
                 at += rt * rh * rw;
             }
         }
