@@ -27,8 +27,8 @@
 //   warps 1, 3   the bias table that the score launch after this one reads, where it is asked for
 //   8 or 16      epilogue warps, two or four per lane quarter with a part of the columns each; their sums start from the bias,
 //                whose loads pass while the tile is computed. Scores, whose tiles have few slices for their 128 x 128
-//                biases and stores, take four warps a quarter (104k rows, 24 heads: 93 us; two: 96), gradients two (96 us;
-//                four: 102)
+//                biases and stores, take four warps a quarter (104k rows, 24 heads: 93 us; two: 96), gradients two (uncut
+//                along K 96 us; four: 102)
 //   12           split warps, three groups with a stage each that take the slices in turn, so that one group's waits pass while
 //                others work. Thread i of 128 has row i of both operands: it reads its 32 values of K (rows of K lie in
 //                the 128-byte swizzle, so that 8 lanes' 16-byte pieces fall into 8 different banks; columns are
