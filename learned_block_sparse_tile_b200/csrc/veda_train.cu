@@ -188,12 +188,12 @@ int launch_distill(const DistillArgs& a, cudaStream_t s) {
 }
 
 // Query rows of one chunk of the bias gradient's sums: with all heads as many CTAs for each of 148 SMs as can be
-// resident, but not fewer than eight rows, which a chunk's own start and end cost. Three against two: 819 tiles, 24 heads
-// 28 and 32 us, 1860 tiles, 24 heads 110 and 82; two against one: 3720 tiles, 8 heads 103 and 130, 7320 tiles, 4 heads 231
-// and 205. Over 8192 tiles the kernel without offset sums runs, bound by latency: 14,880 tiles 8.6, 3.2, 2.8 ms with one,
-// three, six.
+// resident (their registers decide), but not fewer than eight rows, which a chunk's own start and end cost. Three against
+// two: 819 tiles, 24 heads 28 and 32 us, 480 tiles (a CTA too many) 24 and 16, 1860 tiles 110 and 82; two against one: 3720
+// tiles, 8 heads 103 and 130, 7320 tiles, 4 heads 231 and 205. Over 8192 tiles the kernel without offset sums runs, bound
+// by latency: 14,880 tiles 8.6, 3.2, 2.8 ms with one, three, six.
 int bias_chunk_rows(int n, int n_heads) {
-    const int resident = n <= 1024 ? 3 : n <= 4096 ? 2 : n <= 8192 ? 1 : 6;  // CTAs on an SM
+    const int resident = n <= 1024 ? (n <= 416 || n > 512 ? 3 : 2) : n <= 4096 ? 2 : n <= 8192 ? 1 : 6;
     const int chunks = std::max(1, std::min(148 * resident / std::max(n_heads, 1), (n + 7) / 8));
     return std::max(1, (n + chunks - 1) / chunks);
 }
