@@ -169,13 +169,16 @@ __global__ void __launch_bounds__(kWarps == 1 ? 128 : 32 * kWarps, kWarps == 1 ?
     if (lane == 0) a.loss[r] = out ? 0.f : w * (gap / zt - logf(zt) + logf(zs));
     if (!a.d_scores) return;
     float* d = a.d_scores + r * a.n;
-    const float c = out ? 0.f : w * a.inv_tau, iz = out ? 0.f : 1.f / zs;
+    const float c = w * a.inv_tau, iz = 1.f / zs;
+    if (out) {  // zeros, whatever the row's scores are (a product with zero would keep a NaN)
+        for (int j = lane; j < a.n; j += kLanes) d[j] = 0.f;
+        return;
+    }
 #pragma unroll
     for (int k = 0; k < kPer; ++k) {
         const int j = lane + kLanes * k;
         if (j < a.n) d[j] = c * (v[k] * iz);
     }
-    if (out) return;
     if constexpr (kWarps == 1) __syncwarp();
     else __syncthreads();
     const float izt = 1.f / zt;
