@@ -424,9 +424,10 @@ int veda_attend_int8_paired(const veda_layout* layout, const void* q_codes, cons
  *
  * All sums are fp32 or wider, nothing is atomic, and two calls on the same inputs give the same bits.
  * Limits of every call here: 16384 video tiles and 65535 heads (VEDA_ERR_UNSUPPORTED beyond). Buffers need
- * 16-byte alignment. The first call that uses a layout on a device uploads its index data (an allocation and a copy
- * that waits): make it before any stream capture. Workspaces are caller-owned scratch, overwritten by the call and free for other use once
- * its kernels have finished; two calls that may overlap need two. */
+ * 16-byte alignment. Outputs and workspaces must not overlap each other or a call's inputs. The first call that uses
+ * a layout on a device uploads its index data (an allocation and a copy that waits): make it before any stream
+ * capture. Workspaces are caller-owned scratch, overwritten by the call and free for other use once its kernels have
+ * finished; two calls that may overlap need two. */
 
 /* The teacher's tile logits: full attention's logits, max-pooled over every pair of video tiles,
  *     teacher[h, i, j] = max over real rows r of tile i and s of tile j of  D^-0.5 q_r . k_s - lse_r.
@@ -491,7 +492,8 @@ int veda_bias_backward(const veda_layout* layout, const float* d_scores, int32_t
  *  tau         temperature, in [1e-30, 1e30].
  *  row_weight  device fp32 [n_heads, n_video], or NULL for 1: w, for instance 1 / rows for a mean.
  *  loss        device fp32 [n_heads, n_video] out.
- *  d_scores    device fp32 [n_heads, n_video, n_video] out, or NULL for the loss alone; must not overlap scores.
+ *  d_scores    device fp32 [n_heads, n_video, n_video] out, or NULL for the loss alone.
+ * Neither output may overlap an input or the other one (VEDA_ERR_INVALID).
  * A row without a target (an empty list, or -inf at every entry of it) or without a score above -inf gets loss 0
  * and gradient 0. A listed -inf carries no mass; a score of -inf has q = 0, and loss +inf where the teacher has
  * mass there. A NaN or +inf score gives a NaN loss and NaN gradients in its row, a NaN or +inf teacher logit a NaN loss

@@ -24,6 +24,17 @@ constexpr int kMaxTrainTiles = 16384;  // the widest row veda_select takes
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 size_t round256(size_t b) { return (b + 255) & ~size_t(255); }
 
+// A buffer of a call; `base` may be null (no buffer, no overlap)
+struct Span {
+    const char* name;
+    const void* base;
+    int64_t bytes;
+};
+bool overlap(const Span& a, const Span& b) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a.base), y = reinterpret_cast<uintptr_t>(b.base);
+    return x && y && x < y + uint64_t(b.bytes) && y < x + uint64_t(a.bytes);
+}
+
 template <class F>
 int guarded(F&& f) {
     try {
@@ -451,10 +462,14 @@ extern "C" int veda_distill(const veda_layout* layout, const float* scores, int3
         DistillArgs a{};
         a.n = layout->desc.n_video;
         a.rows = int64_t(n_heads) * a.n;
-        const char *s0 = reinterpret_cast<const char*>(scores), *d0 = reinterpret_cast<const char*>(d_scores);
-        const int64_t bytes = a.rows * a.n * 4;
-        if (d_scores && d0 < s0 + bytes && s0 < d0 + bytes)
-            return fail(VEDA_ERR_INVALID, "veda_distill: d_scores must not overlap scores");
+        const int64_t row = 4 * a.rows, square = row * a.n, list = row * width;
+        const Span l{"loss", loss, row}, d{"d_scores", d_scores, square};
+        for (const Span& in : {Span{"scores", scores, square}, Span{"t_idx", t_idx, list}, Span{"t_val", t_val, by_column ? square : list},
+                               Span{"t_cnt", t_cnt, row}, Span{"row_weight", row_weight, row}})
+            for (const Span& out : {l, d})
+                if (overlap(out, in))
+                    return fail(VEDA_ERR_INVALID, std::string("veda_distill: ") + out.name + " must not overlap " + in.name);
+        if (overlap(d, l)) return fail(VEDA_ERR_INVALID, "veda_distill: d_scores must not overlap loss");
         DeviceInfo di;
         if (int rc = current_device(&di)) return rc;
         a.scores = scores;
