@@ -233,6 +233,20 @@ int launch_bias_backward(const BiasBackwardArgs& a, int chunks, int n_heads, con
     return launch_status("bias_backward_kernel");
 }
 
+// (the limit is the function's, shared by all host threads: it is set once, for the widest row)
+int launch_bias_wide(const BiasBackwardArgs& a, int chunks, int n_heads, const DeviceInfo& di, cudaStream_t s) {
+    static std::atomic<bool> set[kMaxDevices];
+    if (!set[di.ordinal].load()) {
+        cudaError_t e = cudaFuncSetAttribute(bias_backward_wide_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             kMaxTrainTiles * int(sizeof(float)));
+        if (e != cudaSuccess)
+            return fail(VEDA_ERR_CUDA, std::string("cudaFuncSetAttribute(bias_backward_wide_kernel): ") + cudaGetErrorString(e));
+        set[di.ordinal].store(true);
+    }
+    bias_backward_wide_kernel<<<dim3(chunks, n_heads), 256, a.n * sizeof(float), s>>>(a);
+    return launch_status("bias_backward_wide_kernel");
+}
+
 template <int kPer>
 int launch_bias(bool one_span, const BiasBackwardArgs& a, int chunks, int n_heads, const DeviceInfo& di, cudaStream_t s) {
     return one_span ? launch_bias_backward<kPer, true>(a, chunks, n_heads, di, s)
@@ -417,12 +431,7 @@ extern "C" int veda_bias_backward(const veda_layout* layout, const float* d_scor
         cudaStream_t s = static_cast<cudaStream_t>(stream);
         int rc;
         if (bias_smem(a) > size_t(kBiasMaxSmem) || a.n > 8192) {
-            const int smem = a.n * int(sizeof(float));
-            cudaError_t e = cudaFuncSetAttribute(bias_backward_wide_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-            if (e != cudaSuccess)
-                return fail(VEDA_ERR_CUDA, std::string("cudaFuncSetAttribute(bias_backward_wide_kernel): ") + cudaGetErrorString(e));
-            bias_backward_wide_kernel<<<dim3(chunks, n_heads), 256, smem, s>>>(a);
-            rc = launch_status("bias_backward_wide_kernel");
+            rc = launch_bias_wide(a, chunks, n_heads, di, s);
         } else {
             const bool one = a.n_spans == 1;
             rc = a.n <= 512    ? launch_bias<1>(one, a, chunks, n_heads, di, s)

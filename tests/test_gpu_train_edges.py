@@ -1,5 +1,7 @@
 """The operators that train the tile predictor at the edges of what their documentation allows."""
+import ctypes as C
 import math
+import threading
 
 import pytest
 import torch
@@ -22,6 +24,10 @@ def built():
     L.veda_device_check()
     yield
     assert L.veda_sync_status() == L.VEDA_OK
+
+
+def bytes_(n):
+    return torch.empty(max(n, 256), dtype=torch.uint8, device=DEV)
 
 
 # --------------------------------------------------------------------------------------------- distillation
@@ -62,3 +68,45 @@ def test_distill_rows_left_out_have_no_gradient_whatever_their_scores_are(geomet
     out[0, :3] = out[1, :2] = True
     assert bool((loss[out] == 0).all()) and bool((d[out] == 0).all())
     assert bool(torch.isfinite(loss[~out]).all()) and bool(torch.isfinite(d[~out]).all()) and bool((d[~out] != 0).any(dim=1).all())
+
+
+# ------------------------------------------------------------------------------------------- bias gradient
+
+
+def bias_backward(geo, ds, reach, far):
+    H = ds.shape[0]
+    out = torch.full((H, L.veda_bias_buckets(reach, far)), 7.0, device=DEV)
+    ws = bytes_(L.veda_bias_backward_workspace_bytes(geo.layout, H, reach))
+    L.veda_bias_backward(geo.layout, ds, reach, far, ws, out)
+    assert L.veda_sync_status() == L.VEDA_OK, L.veda_last_error()
+    return out
+
+
+def test_bias_gradient_of_wide_layouts_from_several_threads():
+    # host threads whose layouts need different amounts of shared memory: neither's call is refused
+    jobs = []
+    for n, calls in ((16384, 400), (8200, 3000), (8200, 3000)):
+        geo = Geometry([((n, 1, 1), (1, 1, 128))])
+        ds = randn(n, 1, n, n)
+        want = bias_backward(geo, ds, (2, 1, 1), (9, 2, 2))
+        ws = bytes_(L.veda_bias_backward_workspace_bytes(geo.layout, 1, (2, 1, 1)))
+        jobs.append((geo, ds, ws, torch.empty_like(want), want, calls, torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    problems, start = [], threading.Barrier(len(jobs))
+
+    def work(geo, ds, ws, out, want, calls, stream):
+        args = (geo.layout.handle, ds.data_ptr(), 1, C.byref(L.BiasSpec((2, 1, 1), (9, 2, 2))), ws.data_ptr(), ws.nbytes,
+                out.data_ptr(), C.c_void_p(stream.cuda_stream))
+        call = L.lib().veda_bias_backward
+        start.wait()
+        codes = {call(*args) for _ in range(calls)}  # (the interpreter's lock is free during a call)
+        stream.synchronize()
+        if codes != {L.VEDA_OK} or not torch.equal(out, want):
+            problems.append((geo.n, codes))
+
+    threads = [threading.Thread(target=work, args=job) for job in jobs]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not problems, problems
