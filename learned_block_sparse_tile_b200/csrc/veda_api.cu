@@ -643,7 +643,9 @@ extern "C" int veda_select(const veda_layout* layout, const float* scores, int32
     }
     const size_t smem = size_t(widest) * sizeof(uint32_t);
     if (smem > 48 * 1024) {
-        cudaError_t e = cudaFuncSetAttribute(select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+        // (the limit is the function's, shared by all host threads: always the widest row's, never lowered)
+        cudaError_t e = cudaFuncSetAttribute(select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             kSelectMaxCols * int(sizeof(uint32_t)));
         if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(select_kernel)");
     }
     select_kernel<<<dim3(unsigned(d.n_video), unsigned(n_heads)), kSelectThreads, smem, static_cast<cudaStream_t>(stream)>>>(a);
@@ -728,8 +730,8 @@ static int launch_paired(DeviceState* ds, const AttendMaps& maps, AttendArgs a, 
         const int64_t smem = per_warp * wpb;
         if (smem > 227 * 1024)
             return fail(VEDA_ERR_UNSUPPORTED, "veda_attend_paired: kept lists too wide for the list merge");
-        if (smem > 49152) {
-            e = cudaFuncSetAttribute(pair_units_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+        if (smem > 49152) {  // (the limit is shared by all host threads: always the largest, never lowered)
+            e = cudaFuncSetAttribute(pair_units_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
             if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(pair_units_kernel)");
         }
         pair_units_kernel<<<unsigned((warps + wpb - 1) / wpb), unsigned(32 * wpb), size_t(smem), s>>>(u);

@@ -82,31 +82,54 @@ def bias_backward(geo, ds, reach, far):
     return out
 
 
+def in_threads(jobs):
+    """Runs every job (a C call, its arguments, how often, its stream) on a host thread of its own, all at once, and returns
+    the sets of their status codes. The interpreter's lock is free during a call."""
+    torch.cuda.synchronize()
+    codes, start = [None] * len(jobs), threading.Barrier(len(jobs))
+
+    def work(i, call, args, calls, stream):
+        start.wait()
+        codes[i] = {call(*args) for _ in range(calls)}
+        stream.synchronize()
+
+    threads = [threading.Thread(target=work, args=(i, *job)) for i, job in enumerate(jobs)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    return codes
+
+
 def test_bias_gradient_of_wide_layouts_from_several_threads():
     # host threads whose layouts need different amounts of shared memory: neither's call is refused
-    jobs = []
+    jobs, results, keep = [], [], []
+    spec = L.BiasSpec((2, 1, 1), (9, 2, 2))
     for n, calls in ((16384, 400), (8200, 3000), (8200, 3000)):
         geo = Geometry([((n, 1, 1), (1, 1, 128))])
         ds = randn(n, 1, n, n)
         want = bias_backward(geo, ds, (2, 1, 1), (9, 2, 2))
         ws = bytes_(L.veda_bias_backward_workspace_bytes(geo.layout, 1, (2, 1, 1)))
-        jobs.append((geo, ds, ws, torch.empty_like(want), want, calls, torch.cuda.Stream()))
-    torch.cuda.synchronize()
-    problems, start = [], threading.Barrier(len(jobs))
+        out, stream = torch.empty_like(want), torch.cuda.Stream()
+        keep.append((geo, ds, ws))
+        results.append((out, want))
+        jobs.append((L.lib().veda_bias_backward, (geo.layout.handle, ds.data_ptr(), 1, C.byref(spec), ws.data_ptr(), ws.nbytes,
+                                                  out.data_ptr(), C.c_void_p(stream.cuda_stream)), calls, stream))
+    assert in_threads(jobs) == [{L.VEDA_OK}] * len(jobs)
+    assert all(torch.equal(out, want) for out, want in results)
 
-    def work(geo, ds, ws, out, want, calls, stream):
-        args = (geo.layout.handle, ds.data_ptr(), 1, C.byref(L.BiasSpec((2, 1, 1), (9, 2, 2))), ws.data_ptr(), ws.nbytes,
-                out.data_ptr(), C.c_void_p(stream.cuda_stream))
-        call = L.lib().veda_bias_backward
-        start.wait()
-        codes = {call(*args) for _ in range(calls)}  # (the interpreter's lock is free during a call)
-        stream.synchronize()
-        if codes != {L.VEDA_OK} or not torch.equal(out, want):
-            problems.append((geo.n, codes))
 
-    threads = [threading.Thread(target=work, args=job) for job in jobs]
-    for t in threads:
-        t.start()
-    for t in threads:
-        t.join()
-    assert not problems, problems
+def test_selection_in_wide_layouts_from_several_threads():
+    jobs, results, keep = [], [], []
+    for n, calls in ((16384, 300), (12400, 1500), (12400, 1500)):  # both over the 48 KB that need no opt-in
+        geo = Geometry([((n, 1, 1), (1, 1, 128))], ratio=0.001)
+        scores = randn(n, 1, n, n)
+        want, out = (torch.zeros(1, n, geo.layout.max_kept, dtype=torch.int32, device=DEV) for _ in range(2))
+        cnt, stream = torch.zeros(1, n, dtype=torch.int32, device=DEV), torch.cuda.Stream()
+        L.veda_select(geo.layout, scores, want, cnt)
+        keep.append((geo, scores, cnt))
+        results.append((out, want))
+        jobs.append((L.lib().veda_select, (geo.layout.handle, scores.data_ptr(), 1, out.data_ptr(), cnt.data_ptr(),
+                                           C.c_void_p(stream.cuda_stream)), calls, stream))
+    assert in_threads(jobs) == [{L.VEDA_OK}] * len(jobs)
+    assert all(torch.equal(out, want) for out, want in results)
