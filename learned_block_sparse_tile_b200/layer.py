@@ -8,6 +8,8 @@ device buffers and supplies the stream; every step runs in libveda's kernels.
 """
 from __future__ import annotations
 
+import contextlib
+
 import torch
 
 from . import _lib as L
@@ -105,19 +107,61 @@ class VedaLayer:
         self.launches = ((self.LAUNCHES_PER_GROUP_DIRECT if self.direct else self.LAUNCHES_PER_GROUP) +
                          (self.EXTRA_LAUNCHES_PAIRED if self.paired else 0)) * len(self.groups)
         self.bias_spec = None  # (reach, far) of set_bias
+        self._readers = {}     # streams that have read the parameters, by handle
+        self._changed, self._changed_on = None, None  # the parameters' last change: its event, its stream's handle
         self._side = torch.cuda.Stream(self.device)  # the V gathers
 
     def set_projections(self, proj_q, proj_k):
-        """proj_q, proj_k: fp32 [H, 3D, D] (any device); each group keeps its heads' slices on device."""
-        for g in self.groups:
-            idx = torch.tensor(g["heads_list"], dtype=torch.long)
-            g["proj_q"] = proj_q.index_select(0, idx).to(self.device, torch.float32).contiguous()
-            g["proj_k"] = proj_k.index_select(0, idx).to(self.device, torch.float32).contiguous()
+        """proj_q, proj_k: fp32 [H, 3D, D] (any device); each group keeps its heads' slices on device. As with set_bias,
+        the values change on the current stream: behind the calls made so far, on whatever stream, that read the old
+        ones, and before every later one. Where shapes stay, so do addresses: a captured forward replays with new values."""
+        with self._changing():
+            for g in self.groups:
+                idx = torch.tensor(g["heads_list"], dtype=torch.long)
+                self._put(g, "proj_q", proj_q.index_select(0, idx).to(self.device, torch.float32).contiguous())
+                self._put(g, "proj_k", proj_k.index_select(0, idx).to(self.device, torch.float32).contiguous())
+
+    @contextlib.contextmanager
+    def _changing(self):
+        """Around a change of the parameters on the current stream."""
+        here = torch.cuda.current_stream(self.device)
+        for s in self._readers.values():
+            here.wait_stream(s)
+        try:
+            yield
+        finally:
+            self._changed, self._changed_on = torch.cuda.Event(), here.cuda_stream
+            self._changed.record(here)
+
+    def _reading(self, stream):
+        """Before work on `stream` that reads the parameters. (A capturing stream cannot wait for work outside its graph:
+        the graph's replays are ordered by whoever replays it.)"""
+        s = stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(stream, device=self.device)
+        self._readers.setdefault(s.cuda_stream, s)
+        if self._changed is not None and s.cuda_stream != self._changed_on:
+            with torch.cuda.stream(s):
+                capturing = torch.cuda.is_current_stream_capturing()
+            if not capturing:
+                s.wait_event(self._changed)
+
+    def _put(self, g, key, value):
+        """A group's tensor, in place where its shape stays, else (or with value None) in the old one's stead, whose memory
+        is kept until the streams that may still read it are through."""
+        old = g.get(key)
+        if old is not None and value is not None and old.shape == value.shape:
+            old.copy_(value)
+            return
+        if old is not None:
+            for s in self._readers.values():
+                old.record_stream(s)
+            del g[key]
+        if value is not None:
+            g[key] = value
 
     def set_bias(self, reach=None, far=None, bias=None):
         """A learned relative position bias of the tile scores (veda_score_bias): per-axis (t, h, w) reaches and far
         distances in tiles, and bias fp32 [H, buckets] (any device; veda_bias_buckets gives the number). Selection then
-        ranks score + bias. No arguments: no bias, the scores of veda_score."""
+        ranks score + bias. No arguments: no bias, the scores of veda_score. Streams as in set_projections."""
         if bias is None and (reach is not None or far is not None):
             raise ValueError("VedaLayer.set_bias: reach and far come with a bias")
         buckets = None if bias is None else L.veda_bias_buckets(reach, far)
@@ -126,17 +170,19 @@ class VedaLayer:
         had = self.bias_spec is not None
         self.bias_spec = None if bias is None else (tuple(reach), tuple(far))
         self.launches += ((bias is None) - (not had)) * len(self.groups)  # one launch fewer per group with a bias
-        for g in self.groups:
-            for key in ("bias", "hats", "bias_ws"):
-                g.pop(key, None)
-            if bias is None:
-                continue
-            n, lay = len(g["heads_list"]), g["layout"]
-            idx = torch.tensor(g["heads_list"], dtype=torch.long, device=bias.device)
-            g["bias"] = bias.index_select(0, idx).to(self.device, torch.float32).contiguous()
-            g["hats"] = torch.empty(2, n, lay.n_video, self.dim, dtype=torch.float32, device=self.device)
-            g["bias_ws"] = torch.empty(L.veda_score_bias_workspace_bytes(lay, n, self.dim), dtype=torch.uint8,
-                                       device=self.device)
+        with self._changing():
+            for g in self.groups:
+                if bias is None:
+                    for key in ("bias", "hats", "bias_ws"):
+                        self._put(g, key, None)
+                    continue
+                n, lay = len(g["heads_list"]), g["layout"]
+                idx = torch.tensor(g["heads_list"], dtype=torch.long, device=bias.device)
+                self._put(g, "bias", bias.index_select(0, idx).to(self.device, torch.float32).contiguous())
+                if "hats" not in g:
+                    g["hats"] = torch.empty(2, n, lay.n_video, self.dim, dtype=torch.float32, device=self.device)
+                    g["bias_ws"] = torch.empty(L.veda_score_bias_workspace_bytes(lay, n, self.dim), dtype=torch.uint8,
+                                               device=self.device)
 
     def _score(self, g, stream):
         lay = g["layout"]
@@ -174,8 +220,10 @@ class VedaLayer:
         ``events``: optional dict; CUDA event pairs recorded around each stage are appended under the stage
         names (the page's PhaseTimer): gather_qk, score, select, gather_v and attend on the tile-order path
         (gather_v runs on a second stream, concurrently with score and select; the others on ``stream``),
-        pool_qk, score, select and attend on the gather-free path (all on ``stream``)."""
+        pool_qk, score, select and attend on the gather-free path (all on ``stream``). The layer's buffers are shared
+        by its calls: whoever makes them on several streams orders them."""
         st = stream if stream is not None else torch.cuda.current_stream()
+        self._reading(st)
 
         def mark(name, on):
             if events is None:

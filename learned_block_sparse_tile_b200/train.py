@@ -70,11 +70,13 @@ class PredictorTrainer:
     def step(self, stream=None):
         """(loss, gradients) of the layer's present projections and bias on the batch of the last teach: the mean loss
         over heads and query tiles (a 0-d fp32 cuda tensor) and a dict of fp32 cuda tensors in the layer's head order,
-        proj_q and proj_k [H, 3D, D] and, with a bias, bias [H, buckets]."""
+        proj_q and proj_k [H, 3D, D] and, with a bias, bias [H, buckets]. teach and step share buffers: whoever makes
+        them on several streams orders them, as with every tensor that torch hands out on a stream."""
         layer = self.layer
         if self.state is None:
             raise ValueError("PredictorTrainer.step: call teach first")
         st = stream if stream is not None else torch.cuda.current_stream(layer.device)
+        layer._reading(st)
         spec = layer.bias_spec
         with torch.cuda.stream(st):
             f = lambda *shape: torch.zeros(shape, dtype=torch.float32, device=layer.device)  # noqa: E731
