@@ -117,9 +117,9 @@ class VedaLayer:
         ones, and before every later one. Where shapes stay, so do addresses: a captured forward replays with new values."""
         with self._changing():
             for g in self.groups:
-                idx = torch.tensor(g["heads_list"], dtype=torch.long)
-                self._put(g, "proj_q", proj_q.index_select(0, idx).to(self.device, torch.float32).contiguous())
-                self._put(g, "proj_k", proj_k.index_select(0, idx).to(self.device, torch.float32).contiguous())
+                for key, proj in (("proj_q", proj_q), ("proj_k", proj_k)):
+                    idx = torch.tensor(g["heads_list"], dtype=torch.long, device=proj.device)
+                    self._put(g, key, proj.detach().index_select(0, idx).to(self.device, torch.float32).contiguous())
 
     @contextlib.contextmanager
     def _changing(self):
@@ -178,7 +178,7 @@ class VedaLayer:
                     continue
                 n, lay = len(g["heads_list"]), g["layout"]
                 idx = torch.tensor(g["heads_list"], dtype=torch.long, device=bias.device)
-                self._put(g, "bias", bias.index_select(0, idx).to(self.device, torch.float32).contiguous())
+                self._put(g, "bias", bias.detach().index_select(0, idx).to(self.device, torch.float32).contiguous())
                 if "hats" not in g:
                     g["hats"] = torch.empty(2, n, lay.n_video, self.dim, dtype=torch.float32, device=self.device)
                     g["bias_ws"] = torch.empty(L.veda_score_bias_workspace_bytes(lay, n, self.dim), dtype=torch.uint8,

@@ -118,3 +118,16 @@ def test_a_captured_forward_replays_with_new_parameters():
         torch.cuda.synchronize()
         assert torch.equal(out, m.outs[i])
     assert L.veda_sync_status() == L.VEDA_OK
+
+
+def test_parameters_from_the_device():
+    # as an optimizer leaves them: on the GPU, leaves that require a gradient
+    m = Made()
+    for i in (0, 1):
+        pq, pk, table = (x.cuda().requires_grad_() for x in m.sets[i])
+        m.layer.set_projections(pq, pk)
+        m.layer.set_bias(REACH, FAR, table)
+        out = m.forward()
+        torch.cuda.synchronize()
+        assert torch.equal(out, m.outs[i]) and not out.requires_grad
+        assert not any(g[key].requires_grad for g in m.layer.groups for key in ("proj_q", "proj_k", "bias"))
