@@ -467,6 +467,9 @@ int veda_bias_index(const veda_layout* layout, const veda_bias_spec* spec, int32
  *  workspace   at least veda_score_bias_workspace_bytes().
  * Other arguments and errors as veda_score. */
 size_t veda_score_bias_workspace_bytes(const veda_layout* layout, int32_t n_heads, int32_t dim);
+/* Kernels that one veda_score_bias call launches on the current device (host): 2, or 3 where the projections are cut
+ * along K to fill the SMs. */
+int veda_score_bias_launches(const veda_layout* layout, int32_t n_heads, int32_t dim, int32_t* launches);
 int veda_score_bias(const veda_layout* layout, const float* feats_q, const float* feats_k, int32_t n_heads, int32_t dim,
                     const float* proj_q, const float* proj_k, const veda_bias_spec* spec, const float* bias, float* hats,
                     void* workspace, size_t workspace_bytes, float* scores, void* stream);

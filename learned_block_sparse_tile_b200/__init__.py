@@ -14,7 +14,7 @@ from ._lib import (  # noqa: F401
     veda_layout_export_direct, veda_pool, veda_attend_direct,
     veda_teacher, veda_bias_buckets, veda_bias_index, veda_score_bias_workspace_bytes, veda_score_bias,
     veda_bias_backward_workspace_bytes, veda_bias_backward, veda_distill, veda_score_backward_workspace_bytes,
-    veda_score_backward,
+    veda_score_backward, veda_score_bias_launches,
 )
 from .layer import VedaLayer  # noqa: F401
 from .pipeline import HostPipeline  # noqa: F401

@@ -29,7 +29,7 @@ EXPORTS = [
     "veda_attend_fp8_paired", "veda_attend_int8_paired",
     "veda_teacher", "veda_bias_buckets", "veda_bias_index", "veda_score_bias_workspace_bytes", "veda_score_bias",
     "veda_bias_backward_workspace_bytes", "veda_bias_backward", "veda_distill", "veda_score_backward_workspace_bytes",
-    "veda_score_backward",
+    "veda_score_backward", "veda_score_bias_launches",
 ]
 
 VEDA_SEG_OTHER, VEDA_SEG_VIDEO, VEDA_SEG_COND, VEDA_SEG_REF_IMG = range(4)
@@ -144,6 +144,7 @@ def lib():
         L.veda_bias_buckets.argtypes = [spec, C.POINTER(C.c_int32)]
         L.veda_bias_index.argtypes = [vp, spec, p]
         L.veda_score_bias_workspace_bytes.argtypes = [vp, i32, i32]
+        L.veda_score_bias_launches.argtypes = [vp, i32, i32, C.POINTER(C.c_int32)]
         L.veda_score_bias.argtypes = [vp, p, p, i32, i32, p, p, spec, p, p, p, C.c_size_t, p, vp]
         L.veda_bias_backward_workspace_bytes.argtypes = [vp, i32, spec]
         L.veda_bias_backward.argtypes = [vp, p, i32, spec, p, C.c_size_t, p, vp]
@@ -477,6 +478,13 @@ def veda_bias_index(layout, reach, far):
 def veda_score_bias_workspace_bytes(layout, n_heads, dim, reach=None):
     """Bytes of workspace veda_score_bias needs (``reach`` does not change it)."""
     return int(lib().veda_score_bias_workspace_bytes(layout.handle, n_heads, dim))
+
+
+def veda_score_bias_launches(layout, n_heads, dim):
+    """Kernels that one veda_score_bias call launches on the current device."""
+    n = C.c_int32()
+    _check(lib().veda_score_bias_launches(layout.handle, n_heads, dim, C.byref(n)))
+    return n.value
 
 
 def veda_score_bias(layout, feats_q, feats_k, proj_q, proj_k, reach, far, bias, hats, workspace, scores, stream=None):

@@ -139,6 +139,18 @@ int operand_maps(CUtensorMap* m, const train::Operand& o, int K, int batches) {
 constexpr int kSplitUnits = 148, kSplitSlices = 4, kJoinSlices = 6;
 constexpr size_t kSplitBytes = size_t(kSplitUnits) * train::kBM * train::kBN * sizeof(float);  // parts of split tiles
 
+// Tiles past whole rounds of CTAs are cut along K into as many parts as CTAs are left, of at least kSplitSlices slices,
+// when that shortens the last round by more than joining the parts takes (about kJoinSlices slices' time). 819 tiles,
+// D 128, both gradients: 24 heads 96 -> 93 us, 8 heads 50 -> 46, 1 head 46 -> 24. More than one part takes a launch more.
+int parts_along_k(int64_t tiles, int K, int sms) {
+    const int nk = (K + train::kBK - 1) / train::kBK, rest = int(tiles % sms);
+    const int parts = rest ? std::min(std::min(sms, kSplitUnits) / rest, nk / kSplitSlices) : 1;
+    return parts < 2 || nk - (nk + parts - 1) / parts < kJoinSlices ? 1 : parts;
+}
+int64_t tiles_of(int sets, int batches, int M, int N) {
+    return int64_t(sets) * batches * ((M + train::kBM - 1) / train::kBM) * ((N + train::kBN - 1) / train::kBN);
+}
+
 // `after`: the launch before it on the stream is one of this call's, and its start may overlap that one's end
 template <int kParts>
 int launch_gemm(const char* what, train::Args a, const BiasExpand& expand, bool after, const DeviceInfo& di, cudaStream_t s) {
@@ -151,14 +163,10 @@ int launch_gemm(const char* what, train::Args a, const BiasExpand& expand, bool 
     }
     a.tiles_m = (a.M + train::kBM - 1) / train::kBM;
     a.tiles_n = (a.N + train::kBN - 1) / train::kBN;
-    const int64_t tiles = int64_t(a.n_sets) * a.nb * a.tiles_m * a.tiles_n;
+    const int64_t tiles = tiles_of(a.n_sets, a.nb, a.M, a.N);
     if (tiles > INT32_MAX - kSplitUnits) return fail(VEDA_ERR_UNSUPPORTED, std::string(what) + ": too many tiles for one launch");
-    // Tiles past whole rounds of CTAs are cut along K into as many parts as CTAs are left, of at least kSplitSlices slices,
-    // when that shortens the last round by more than joining the parts takes (about kJoinSlices slices' time). 819 tiles,
-    // D 128, both gradients: 24 heads 96 -> 93 us, 8 heads 50 -> 46, 1 head 46 -> 24.
-    const int nk = (a.K + train::kBK - 1) / train::kBK, rest = int(tiles % di.sms);
-    a.parts = rest && a.partial ? std::min(std::min(di.sms, kSplitUnits) / rest, nk / kSplitSlices) : 1;
-    if (a.parts < 2 || nk - (nk + a.parts - 1) / a.parts < kJoinSlices) a.parts = 1;
+    const int rest = int(tiles % di.sms);
+    a.parts = a.partial ? parts_along_k(tiles, a.K, di.sms) : 1;
     a.full = int(tiles) - (a.parts > 1 ? rest : 0);
     a.n_units = a.full + (a.parts > 1 ? rest * a.parts : 0);
     a.timeout_ns = wait_timeout_ns();
@@ -329,6 +337,20 @@ extern "C" int veda_teacher(const veda_layout* layout, const void* q_t, const vo
 extern "C" size_t veda_score_bias_workspace_bytes(const veda_layout* layout, int32_t n_heads, int32_t dim) {
     if (!layout || n_heads <= 0 || dim <= 0) return 0;
     return kSplitBytes + round256(size_t(n_heads) * size_t(layout->bias_offsets + 2) * sizeof(float));
+}
+
+extern "C" int veda_score_bias_launches(const veda_layout* layout, int32_t n_heads, int32_t dim, int32_t* launches) {
+    return guarded([&] {
+        clear_error();
+        if (!layout || !launches) return fail(VEDA_ERR_INVALID, "veda_score_bias_launches: NULL argument");
+        if (int rc = check_heads("veda_score_bias_launches", n_heads, dim)) return rc;
+        if (int rc = check_size("veda_score_bias_launches", layout, n_heads)) return rc;
+        DeviceInfo di;
+        if (int rc = current_device(&di)) return rc;
+        // the projections, cut or not, and the logits
+        *launches = 2 + (parts_along_k(tiles_of(2, n_heads, dim, layout->desc.n_video), 3 * dim, di.sms) > 1);
+        return VEDA_OK;
+    });
 }
 
 extern "C" int veda_score_bias(const veda_layout* layout, const float* feats_q, const float* feats_k, int32_t n_heads,

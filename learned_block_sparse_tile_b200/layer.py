@@ -42,6 +42,7 @@ class VedaLayer:
     # tile-order path: gather q, gather k, the projections' transpose, 2 score GEMMs, select, gather v, attend
     LAUNCHES_PER_GROUP = 8
     LAUNCHES_PER_GROUP_DIRECT = 7  # gather-free path: pool q, pool k, transpose, 2 score GEMMs, select, attend
+    LAUNCHES_SCORE = 3  # of these the transpose and the 2 score GEMMs; with a bias veda_score_bias_launches
     EXTRA_LAUNCHES_PAIRED = 2  # the paired attend adds the list merge and the (usually empty) redo pass
 
     def __init__(self, seq_len, ref_spans, target, head_shapes, budgets, heads, dim, device="cuda", fp8_qk=False,
@@ -104,8 +105,9 @@ class VedaLayer:
                 g.update(q_row_sq=None, k_max_sq=None)
             g.update(pair_ws=L.paired_workspace(lay, n, dev) if self.paired else None)
             self.groups.append(g)
-        self.launches = ((self.LAUNCHES_PER_GROUP_DIRECT if self.direct else self.LAUNCHES_PER_GROUP) +
-                         (self.EXTRA_LAUNCHES_PAIRED if self.paired else 0)) * len(self.groups)
+        self._launches_plain = ((self.LAUNCHES_PER_GROUP_DIRECT if self.direct else self.LAUNCHES_PER_GROUP) +
+                                (self.EXTRA_LAUNCHES_PAIRED if self.paired else 0)) * len(self.groups)
+        self.launches = self._launches_plain  # kernels one forward launches
         self.bias_spec = None  # (reach, far) of set_bias
         self._readers = {}     # streams that have read the parameters, by handle
         self._changed, self._changed_on = None, None  # the parameters' last change: its event, its stream's handle
@@ -167,9 +169,6 @@ class VedaLayer:
         buckets = None if bias is None else L.veda_bias_buckets(reach, far)
         if bias is not None and tuple(bias.shape) != (self.heads, buckets):
             raise ValueError(f"VedaLayer.set_bias: bias must be [{self.heads}, {buckets}], not {tuple(bias.shape)}")
-        had = self.bias_spec is not None
-        self.bias_spec = None if bias is None else (tuple(reach), tuple(far))
-        self.launches += ((bias is None) - (not had)) * len(self.groups)  # one launch fewer per group with a bias
         with self._changing():
             for g in self.groups:
                 if bias is None:
@@ -183,6 +182,12 @@ class VedaLayer:
                     g["hats"] = torch.empty(2, n, lay.n_video, self.dim, dtype=torch.float32, device=self.device)
                     g["bias_ws"] = torch.empty(L.veda_score_bias_workspace_bytes(lay, n, self.dim), dtype=torch.uint8,
                                                device=self.device)
+        self.bias_spec = None if bias is None else (tuple(reach), tuple(far))
+        self.launches = self._launches_plain
+        if bias is not None:
+            with torch.cuda.device(self.device):
+                self.launches += sum(L.veda_score_bias_launches(g["layout"], len(g["heads_list"]), self.dim) -
+                                     self.LAUNCHES_SCORE for g in self.groups)
 
     def _score(self, g, stream):
         lay = g["layout"]

@@ -1,4 +1,8 @@
-"""A layer's parameters set while work that reads them is queued on other streams, and behind a captured forward."""
+"""A layer's parameters set while work that reads them is queued on other streams, and behind a captured forward; the
+launches it counts."""
+import ctypes as C
+import math
+
 import pytest
 import torch
 
@@ -131,3 +135,40 @@ def test_parameters_from_the_device():
         torch.cuda.synchronize()
         assert torch.equal(out, m.outs[i]) and not out.requires_grad
         assert not any(g[key].requires_grad for g in m.layer.groups for key in ("proj_q", "proj_k", "bias"))
+
+
+def kernel_nodes(call):
+    """Kernels that ``call`` launches, counted in a captured graph."""
+    call()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph(keep_graph=True)
+    with torch.cuda.graph(graph):
+        call()
+    rt = C.CDLL("libcudart.so.12")
+    raw, count = C.c_void_p(graph.raw_cuda_graph()), C.c_size_t()
+    assert rt.cudaGraphGetNodes(raw, None, C.byref(count)) == 0
+    nodes = (C.c_void_p * count.value)()
+    assert rt.cudaGraphGetNodes(raw, nodes, C.byref(count)) == 0
+    kernels = 0
+    for node in nodes:
+        kind = C.c_int()
+        assert rt.cudaGraphNodeGetType(C.c_void_p(node), C.byref(kind)) == 0
+        kernels += kind.value == 0
+    return kernels
+
+
+@pytest.mark.parametrize("dim,heads,grid", [(64, 2, (8, 16, 16)), (128, 2, (8, 16, 16)), (128, 40, (8, 16, 16)), (128, 3, (8, 48, 48))])
+def test_a_layer_counts_the_launches_it_makes(dim, heads, grid):
+    seq = math.prod(grid)
+    layer = VedaLayer(seq, (), (0, grid), ((2, 8, 8),) * heads, ((0.3, None), (1.0, None)), heads, dim)
+    layer.set_projections(*(torch.randn(heads, 3 * dim, dim) / math.sqrt(3 * dim) for _ in range(2)))
+    q, k, v = (torch.randn(seq, heads, dim, device="cuda").to(torch.bfloat16) for _ in range(3))
+    out = torch.empty_like(q)
+    plain = kernel_nodes(lambda: layer.forward(q, k, v, out))
+    assert layer.launches == plain
+    table = torch.zeros(heads, L.veda_bias_buckets((3, 3, 3), (8, 8, 8)))
+    for _ in range(2):
+        layer.set_bias((3, 3, 3), (8, 8, 8), table)
+        assert layer.launches == kernel_nodes(lambda: layer.forward(q, k, v, out))
+    layer.set_bias()
+    assert layer.launches == plain == kernel_nodes(lambda: layer.forward(q, k, v, out))
