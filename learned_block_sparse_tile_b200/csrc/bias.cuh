@@ -122,7 +122,8 @@ __device__ __forceinline__ void bias_interval(const int* starts, int reach, int 
 // every sum is added up in row order. The loads run kDepth rows ahead in registers, because the rows' own work is short:
 // an addition in shared memory and a barrier; a warp waits for its newer loads with its older ones, so they cover the
 // latency of L2 and not of memory, and one thread asks for the chunk's next rows, a run of memory, in L2 further ahead
-// (104k rows, 24 heads, from HBM: 44 -> 32 us). At the end each bucket is the sum of a box of offsets. Bound by the chain
+// (104k rows, 24 heads, from HBM: 44 -> 32 us). At the end each bucket is the sum of a box of offsets, taken axis by axis:
+// a box may hold nearly all offsets, and one chain of them would lose what a few long ones do not. Bound by the chain
 // of shared-memory addition and barrier, with up to three CTAs on an SM taking turns (104k, 24 heads: 28 us from HBM, 23
 // from L2; two CTAs: 32 and 24; two sets of sums and a barrier for each two rows gain nothing: 29 and 23); the floor is
 // reading d_scores once. With two values a thread the registers are held to three CTAs of any size (960 tiles, 24 heads: 36
@@ -219,10 +220,16 @@ __global__ void __launch_bounds__(512, kPer == 2 ? 3 : kPer <= 4 ? 2 : 1) bias_b
                 bias_interval(a.b.starts[0], a.b.reach[0], b / (iw * ih), g.y - 1, rt, t0, t1);
                 bias_interval(a.b.starts[1], a.b.reach[1], (b / iw) % ih, g.z - 1, rh, h0, h1);
                 bias_interval(a.b.starts[2], a.b.reach[2], b % iw, g.w - 1, rw, w0, w1);
-                for (int h = h0; h < h1; ++h)
-                    for (int w = w0; w < w1; ++w)
+                for (int h = h0; h < h1; ++h) {
+                    float plane = 0.f;
+                    for (int w = w0; w < w1; ++w) {
+                        float run = 0.f;
 #pragma unroll 4
-                        for (int t = t0; t < t1; ++t) sum += at[(h * rw + w) * rt + t];
+                        for (int t = t0; t < t1; ++t) run += at[(h * rw + w) * rt + t];
+                        plane += run;
+                    }
+                    sum += plane;
+                }
                 at += rt * rh * rw;
             }
         }
@@ -261,9 +268,15 @@ __global__ void __launch_bounds__(256) bias_backward_wide_kernel(const BiasBackw
                 bias_interval(a.b.starts[0], a.b.reach[0], b / (nw * nh), p.y, g.y, t0, t1);
                 bias_interval(a.b.starts[1], a.b.reach[1], (b / nw) % nh, p.z, g.z, h0, h1);
                 bias_interval(a.b.starts[2], a.b.reach[2], b % nw, p.w, g.w, w0, w1);
-                for (int h = h0; h < h1; ++h)
-                    for (int w = w0; w < w1; ++w)
-                        for (int t = t0; t < t1; ++t) sum += row[g.x + (h * g.w + w) * g.y + t];
+                for (int h = h0; h < h1; ++h) {
+                    float plane = 0.f;
+                    for (int w = w0; w < w1; ++w) {
+                        float run = 0.f;
+                        for (int t = t0; t < t1; ++t) run += row[g.x + (h * g.w + w) * g.y + t];
+                        plane += run;
+                    }
+                    sum += plane;
+                }
             }
             acc[u] += sum;
         }
@@ -275,7 +288,7 @@ __global__ void __launch_bounds__(256) bias_backward_wide_kernel(const BiasBackw
     }
 }
 
-// d_bias[head][b] = the chunks' sums, added in chunk order, eight loads at a time (a programmatic dependent launch)
+// d_bias[head][b] = the chunks' sums, eight loads at a time, added as pairs and eight by eight (a programmatic dependent launch)
 __global__ void __launch_bounds__(128) bias_reduce_kernel(const float* partial, float* d_bias, int chunks, int buckets) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int b = blockIdx.x * 128 + threadIdx.x;
@@ -286,8 +299,7 @@ __global__ void __launch_bounds__(128) bias_reduce_kernel(const float* partial, 
         float v[8];
 #pragma unroll
         for (int x = 0; x < 8; ++x) v[x] = c + x < chunks ? p[int64_t(c + x) * buckets] : 0.f;
-#pragma unroll
-        for (int x = 0; x < 8; ++x) sum += v[x];
+        sum += ((v[0] + v[1]) + (v[2] + v[3])) + ((v[4] + v[5]) + (v[6] + v[7]));
     }
     d_bias[int64_t(blockIdx.y) * buckets + b] = sum;
 }

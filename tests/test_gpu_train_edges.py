@@ -10,7 +10,7 @@ from learned_block_sparse_tile_b200 import _lib as L
 from learned_block_sparse_tile_b200 import build as B
 
 import train_util as T
-from train_util import DEV, Geometry, randn
+from train_util import DEV, EPS, Geometry, randn
 
 pytestmark = pytest.mark.gpu
 
@@ -80,6 +80,41 @@ def bias_backward(geo, ds, reach, far):
     L.veda_bias_backward(geo.layout, ds, reach, far, ws, out)
     assert L.veda_sync_status() == L.VEDA_OK, L.veda_last_error()
     return out
+
+
+def bucket_sums(geo, reach, far, x):
+    """64-bit sums of each bucket, head by head."""
+    index = torch.as_tensor(L.veda_bias_index(geo.layout, reach, far), device=DEV).long().reshape(-1)
+    total = L.veda_bias_buckets(reach, far)
+    return torch.stack([torch.zeros(total, dtype=torch.float64, device=DEV).index_add_(0, index, h.double().reshape(-1)) for h in x])
+
+
+@pytest.mark.parametrize("spans", [[((13, 48, 84), (1, 8, 16))], [((61, 45, 80), (8, 1, 16))], [((16, 128, 256), (1, 8, 16))],
+                                   [((5, 45, 80), (1, 8, 16)), ((2, 16, 16), (2, 8, 8))]])
+@pytest.mark.parametrize("where", ["first", "cross"])
+def test_bias_gradient_of_a_bucket_of_many_offsets(spans, where):
+    # One value is so large that the others, added to it one by one in fp32, would all be lost. It is met first in its bucket:
+    # the offset of the last query and the first key.
+    if where == "cross" and len(spans) == 1:
+        pytest.skip("one span")
+    geo, reach, far = Geometry(spans), (1, 1, 1), (2, 2, 2)
+    n = geo.n
+    ds = torch.ones(1, n, n, device=DEV)
+    first = math.prod(-(-g // b) for g, b in zip(*spans[0]))  # tiles of the first span
+    ds[0, first - 1 if where == "first" else n - 1, 0] = 2.0 ** 28
+    got = bias_backward(geo, ds, reach, far).double()
+    want = bucket_sums(geo, reach, far, ds)
+    # additions that a value passes through: a chunk's rows (fewer than 64 up to 8,192 tiles), a run of offsets along each of
+    # the three axes, the spans, the chunks (eight by eight, fewer than 64 times); across spans a thread's values (fewer
+    # than 16 a row), the lanes and the warps in the place of the runs
+    runs = sum(2 * -(-g // b) - 1 for g, b in zip(*spans[0]))
+    adds = (64 + runs if where == "first" else 64 * 16 + 5 + 16) + len(spans) + 64
+    index = torch.as_tensor(L.veda_bias_index(geo.layout, reach, far), device=DEV)
+    big = int(index[first - 1 if where == "first" else n - 1, 0])
+    # only the sum that holds the large value is that coarse: ones are exact
+    assert float((got[0, big] - want[0, big]).abs()) <= adds * EPS * float(want[0, big])
+    rest = torch.arange(got.shape[1], device=DEV) != big
+    assert float(((got - want).abs() - EPS * want)[0, rest].max()) <= 0
 
 
 def in_threads(jobs):
