@@ -16,6 +16,7 @@ pytestmark = pytest.mark.gpu
 
 REFS = dict(spans=[((2, 16, 16), (2, 8, 8)), ((1, 9, 21), (1, 8, 16)), ((6, 16, 24), (8, 4, 4))], text=150, gap=3)
 LINE1500 = dict(spans=[((1500, 1, 1), (1, 1, 128))])
+SMEM = 227 * 1024  # a CTA's shared memory
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -115,6 +116,30 @@ def test_bias_gradient_of_a_bucket_of_many_offsets(spans, where):
     assert float((got[0, big] - want[0, big]).abs()) <= adds * EPS * float(want[0, big])
     rest = torch.arange(got.shape[1], device=DEV) != big
     assert float(((got - want).abs() - EPS * want)[0, rest].max()) <= 0
+
+
+def offsets_of(spans):
+    """Entries of the table of every offset: (2 T - 1)(2 H - 1)(2 W - 1) of each span's array of tiles."""
+    return sum(math.prod(2 * -(-g // b) - 1 for g, b in zip(grid, box)) for grid, box in spans)
+
+
+@pytest.mark.parametrize("spans,heads,reach,far", [
+    ([((20, 160, 320), (1, 8, 16))], 2, (4, 4, 6), (16, 16, 32)),                          # 20 x 20 x 20 tiles: too many offsets
+    ([((20, 160, 320), (1, 8, 16)), ((4, 64, 64), (2, 8, 8))], 2, (3, 5, 2), (8, 11, 9)),  # and a second span
+    ([((3, 24, 40), (1, 8, 16)), ((21, 160, 320), (1, 8, 16)), ((2, 16, 16), (2, 8, 8))], 1, (2, 3, 4), (9, 7, 12)),
+    ([((90, 8, 1600), (1, 8, 16))], 2, (16, 1, 8), (64, 2, 32)),                           # more than 8,192 tiles, one along h
+    ([((20, 160, 320), (1, 8, 16)), ((1, 8, 16), (1, 8, 16))], 1, (1, 1, 1), (2, 2, 2)),   # one bucket for all offsets
+])
+def test_bias_gradient_without_offset_sums(spans, heads, reach, far):
+    geo = Geometry(spans)
+    # this is what sends a layout to the kernel that sums boxes of each row
+    assert 4 * offsets_of(spans) > SMEM or geo.n > 8192
+    ds = randn(1, heads, geo.n, geo.n)
+    got, want = bias_backward(geo, ds, reach, far), bucket_sums(geo, reach, far, ds)
+    # a value passes through fewer than 2 n + 64 fp32 additions: its row's box, the chunk's rows, the chunks
+    over = (got.double() - want).abs() - (2 * geo.n + 64) * EPS * bucket_sums(geo, reach, far, ds.abs())
+    assert float(over.max()) <= 0
+    assert torch.equal(bias_backward(geo, ds, reach, far), got)
 
 
 def in_threads(jobs):
