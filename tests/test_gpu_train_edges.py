@@ -10,7 +10,7 @@ from learned_block_sparse_tile_b200 import _lib as L
 from learned_block_sparse_tile_b200 import build as B
 
 import train_util as T
-from train_util import DEV, EPS, Geometry, randn
+from train_util import DEV, EPS, SPLIT, Geometry, randn
 
 pytestmark = pytest.mark.gpu
 
@@ -193,3 +193,118 @@ def test_selection_in_wide_layouts_from_several_threads():
                                            C.c_void_p(stream.cuda_stream)), calls, stream))
     assert in_threads(jobs) == [{L.VEDA_OK}] * len(jobs)
     assert all(torch.equal(out, want) for out, want in results)
+
+
+# ------------------------------------------------------------------- values that are not finite, and the largest
+
+
+def feats(seed, heads, n, dim):
+    return torch.cat([0.3 * randn(seed, heads, n, dim), 2.4 + 0.4 * randn(seed + 1, heads, n, dim),
+                      -2.4 + 0.4 * randn(seed + 2, heads, n, dim)], dim=2).contiguous()
+
+
+def projections(seed, heads, dim):
+    return randn(seed, heads, 3 * dim, dim) / math.sqrt(3 * dim)
+
+
+LARGEST = torch.finfo(torch.float32).max
+
+
+def magnitude(a, b):
+    """Sums of the finite values' products, without signs."""
+    return torch.nan_to_num(a, nan=0.0, posinf=0.0, neginf=0.0).abs() @ torch.nan_to_num(b, nan=0.0, posinf=0.0, neginf=0.0).abs()
+
+
+def agrees(got, want, size, tol):
+    """``got`` holds the 64-bit ``want`` within tol, NaN and infinities where want has them; returns how many those are.
+    Passed over: sums whose finite terms alone can pass the type's range (size), which an fp32 sum may leave and not come
+    back to."""
+    seen = size < LARGEST / 2
+    got, want = torch.where(seen, got.double(), 0.0), torch.where(seen, want, 0.0)
+    odd = ~torch.isfinite(want)
+    assert torch.equal(torch.isnan(got), torch.isnan(want))
+    assert torch.equal(got[odd & ~torch.isnan(want)], want[odd & ~torch.isnan(want)])
+    assert float((torch.where(odd, 0.0, (got - want).abs()) - torch.where(seen, tol, 0.0)).max()) <= 0
+    return int(odd.sum())
+
+
+@pytest.mark.parametrize("dim,heads", [(64, 2), (128, 1), (128, 40)])  # whole tiles; cut along K; whole tiles of 128
+def test_scores_of_values_that_are_not_finite(dim, heads):
+    geo, reach, far = Geometry(**REFS), (3, 3, 3), (8, 8, 8)
+    n = geo.n
+    fq, fk = feats(1, heads, n, dim), feats(4, heads, n, dim)
+    pq, pk = projections(7, heads, dim), projections(8, heads, dim)
+    fq[0, 1, 5] = math.inf
+    fq[0, 2, 3 * dim - 1] = -math.inf
+    fq[0, 4, 7] = LARGEST           # finite, and so are its products with entries below one
+    fk[0, 3, dim + 1] = math.nan
+    fk[0, 5, 2] = -LARGEST
+    fk[0, 6, 9], fk[0, 6, 10] = math.inf, -math.inf
+    pk[heads - 1, dim + 3, 11] = math.inf
+    pk[heads - 1, 2, 12] = LARGEST
+    hats = torch.full((2, heads, n, dim), 7.0, device=DEV)
+    scores = torch.full((heads, n, n), 7.0, device=DEV)
+    bias = randn(9, heads, L.veda_bias_buckets(reach, far))
+    bias[:, 0] = -math.inf
+    ws = bytes_(L.veda_score_bias_workspace_bytes(geo.layout, heads, dim))
+    L.veda_score_bias(geo.layout, fq, fk, pq, pk, reach, far, bias, hats, ws, scores)
+    assert L.veda_sync_status() == L.VEDA_OK
+    eye = torch.eye(3 * dim, dim, dtype=torch.float64, device=DEV)
+    found = 0
+    for got, f, p in ((hats[0], fq, pq), (hats[1], fk, pk)):
+        f, p = f.double(), p.double() + eye
+        size = magnitude(f, p.abs() + eye)
+        found += agrees(got, f @ p, size, (SPLIT + (3 * dim + 9) * 2 * EPS) * size)
+    assert found > 2 * dim
+    huge = hats[0, 0, 4].abs() > 1e36  # (the finite one's row)
+    assert int((huge & torch.isfinite(hats[0, 0, 4])).sum()) > dim // 2
+    index = torch.as_tensor(L.veda_bias_index(geo.layout, reach, far), device=DEV).long()
+    b = bias.double()[:, index]
+    q, k = hats.double()
+    size = magnitude(q, k.transpose(1, 2))
+    # (rows that hold values of 2^11 or more on one side and infinities on the other give infinities or NaN)
+    far_apart = (torch.isinf(q).any(2)[:, :, None] & (k.abs() >= 2048).any(2)[:, None]) | \
+        ((q.abs() >= 2048).any(2)[:, :, None] & torch.isinf(k).any(2)[:, None])
+    want = q @ k.transpose(1, 2) / math.sqrt(dim) + b
+    assert not bool(torch.isfinite(scores[far_apart]).any())
+    tol = (SPLIT + (dim + 12) * 2 * EPS) * size + 4 * EPS * torch.nan_to_num(b, neginf=0.0).abs()
+    found = agrees(torch.where(far_apart, 0.0, scores), torch.where(far_apart, 0.0, want), size, tol)
+    assert found > n and bool(torch.isnan(want).any()) and bool((want == -math.inf).any())
+    # the rows and columns of the first head without such a value: scores as always
+    rows = torch.tensor([0] + list(range(7, n)), device=DEV)
+    if heads > 1:
+        assert bool((torch.isfinite(scores[0, rows][:, rows]) | (b[0, rows][:, rows] == -math.inf)).all())
+
+
+@pytest.mark.parametrize("spans,dim,heads", [(REFS["spans"], 64, 2), (REFS["spans"], 128, 1), ([((15, 24, 42), (1, 8, 16))], 128, 1),
+                                             ([((5, 45, 80), (1, 8, 16))], 64, 3), ([((13, 48, 84), (1, 8, 16))], 128, 1)])
+def test_projection_gradients_of_values_that_are_not_finite(spans, dim, heads):
+    geo = Geometry(spans)
+    n = geo.n
+    fq, fk, hats = feats(1, heads, n, dim), feats(4, heads, n, dim), randn(7, 2, heads, n, dim)
+    ds = torch.softmax(2 * randn(9, heads, n, n), 2) - torch.softmax(4 * randn(10, heads, n, n), 2)
+    for case in range(4):
+        f, h, g = fq.clone(), hats.clone(), ds.clone()
+        if case == 0:
+            g[0, 3, n - 2] = math.inf       # one infinite gradient: infinities of the signs that its features give
+        elif case == 1:
+            g[heads - 1, n - 1, 0] = LARGEST
+            h[1, heads - 1, 0] *= 1e-3      # (its products stay in range)
+            h[0, heads - 1, n - 1] *= 1e-3
+        elif case == 2:
+            f[0, 1, 5], f[0, 2, 6] = -math.inf, math.nan
+        else:
+            h[1, 0, 4, 7] = math.inf
+        out = [torch.full((heads, 3 * dim, dim), 7.0, device=DEV) for _ in range(2)]
+        ws = bytes_(L.veda_score_backward_workspace_bytes(geo.layout, heads, dim))
+        L.veda_score_backward(geo.layout, f, fk, h, g, ws, *out)
+        assert L.veda_sync_status() == L.VEDA_OK
+        q, k = h.double()
+        c = 1 / math.sqrt(dim)
+        found = 0
+        for got, x, m, y in ((out[0], f, g.double(), k), (out[1], fk, g.double().transpose(1, 2), q)):
+            dx, ft = c * (m @ y), x.double().transpose(1, 2)
+            bound = c * (SPLIT + (n + 12) * 2 * EPS) * magnitude(m, y)
+            size = magnitude(ft, dx.abs() + bound)
+            found += agrees(got, ft @ dx, size, magnitude(ft, bound) + (SPLIT + (n + 8) * 2 * EPS) * size)
+        assert (found > 0) == (case != 1)
