@@ -109,8 +109,9 @@ class VedaLayer:
                                 (self.EXTRA_LAUNCHES_PAIRED if self.paired else 0)) * len(self.groups)
         self.launches = self._launches_plain  # kernels one forward launches
         self.bias_spec = None  # (reach, far) of set_bias
-        self._readers = {}     # streams that have read the parameters, by handle
-        self._changed, self._changed_on = None, None  # the parameters' last change: its event, its stream's handle
+        # streams that have read the parameters, by handle; of foreign streams the last reads' events
+        self._readers, self._foreign_reads = {}, {}
+        self._changed, self._behind = None, set()  # the parameters' last change, and the streams that have waited for it
         self._side = torch.cuda.Stream(self.device)  # the V gathers
 
     def set_projections(self, proj_q, proj_k):
@@ -129,33 +130,52 @@ class VedaLayer:
         here = torch.cuda.current_stream(self.device)
         for s in self._readers.values():
             here.wait_stream(s)
+        for read in self._foreign_reads.values():
+            here.wait_event(read)
         try:
             yield
         finally:
-            self._changed, self._changed_on = torch.cuda.Event(), here.cuda_stream
+            self._changed = torch.cuda.Event()
             self._changed.record(here)
+            self._behind = {here.cuda_stream} if self._lasting(here) else set()
 
-    def _reading(self, stream):
-        """Before work on `stream` that reads the parameters. (A capturing stream cannot wait for work outside its graph:
-        the graph's replays are ordered by whoever replays it.)"""
+    @staticmethod
+    def _lasting(stream):
+        """torch's own streams live as long as the process; a foreign one's id is its handle."""
+        return stream.cuda_stream == 0 or stream.cuda_stream != stream.stream_id
+
+    @staticmethod
+    def _capturing(stream):
+        with torch.cuda.stream(stream):
+            return torch.cuda.is_current_stream_capturing()
+
+    def _before_read(self, stream):
+        """Before work on `stream` that reads the parameters: waits for their last change. Returns what _after_read takes.
+        (A capturing stream cannot wait for work outside its graph, nor that for it: whoever replays the graph orders it.)"""
         s = stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(stream, device=self.device)
-        self._readers.setdefault(s.cuda_stream, s)
-        if self._changed is not None and s.cuda_stream != self._changed_on:
-            with torch.cuda.stream(s):
-                capturing = torch.cuda.is_current_stream_capturing()
-            if not capturing:
-                s.wait_event(self._changed)
+        if self._changed is not None and s.cuda_stream not in self._behind and not self._capturing(s):
+            s.wait_event(self._changed)
+            if self._lasting(s):
+                self._behind.add(s.cuda_stream)
+        return s
+
+    def _after_read(self, s):
+        """Behind that work: the parameters' next change waits for it."""
+        if self._lasting(s):
+            self._readers[s.cuda_stream] = s
+        elif not self._capturing(s):  # it may be gone by then
+            read = self._foreign_reads.setdefault(s.cuda_stream, torch.cuda.Event())
+            read.record(s)
 
     def _put(self, g, key, value):
         """A group's tensor, in place where its shape stays, else (or with value None) in the old one's stead, whose memory
-        is kept until the streams that may still read it are through."""
+        is free for other use once the current stream, which waits for the readers, has come to here."""
         old = g.get(key)
         if old is not None and value is not None and old.shape == value.shape:
             old.copy_(value)
             return
         if old is not None:
-            for s in self._readers.values():
-                old.record_stream(s)
+            old.record_stream(torch.cuda.current_stream(self.device))
             del g[key]
         if value is not None:
             g[key] = value
@@ -191,11 +211,13 @@ class VedaLayer:
 
     def _score(self, g, stream):
         lay = g["layout"]
+        reading = self._before_read(stream)
         if self.bias_spec is None:
             L.veda_score(lay, g["feats_q"], g["feats_k"], g["proj_q"], g["proj_k"], g["workspace"], g["scores"], stream)
         else:
             L.veda_score_bias(lay, g["feats_q"], g["feats_k"], g["proj_q"], g["proj_k"], *self.bias_spec, g["bias"],
                               g["hats"], g["bias_ws"], g["scores"], stream)
+        self._after_read(reading)
 
     def kept_tiles(self):
         """Total kept (video query tile, key tile) pairs of the last forward, per the page's ``kept``."""
@@ -228,7 +250,6 @@ class VedaLayer:
         pool_qk, score, select and attend on the gather-free path (all on ``stream``). The layer's buffers are shared
         by its calls: whoever makes them on several streams orders them."""
         st = stream if stream is not None else torch.cuda.current_stream()
-        self._reading(st)
 
         def mark(name, on):
             if events is None:

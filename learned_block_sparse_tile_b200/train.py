@@ -76,7 +76,6 @@ class PredictorTrainer:
         if self.state is None:
             raise ValueError("PredictorTrainer.step: call teach first")
         st = stream if stream is not None else torch.cuda.current_stream(layer.device)
-        layer._reading(st)
         spec = layer.bias_spec
         with torch.cuda.stream(st):
             f = lambda *shape: torch.zeros(shape, dtype=torch.float32, device=layer.device)  # noqa: E731
@@ -86,8 +85,10 @@ class PredictorTrainer:
             losses = []
             for g, s in zip(layer.groups, self.state):
                 lay, heads = g["layout"], g["heads"].long()
+                reading = layer._before_read(st)
                 L.veda_score_bias(lay, s["feats_q"], s["feats_k"], g["proj_q"], g["proj_k"], *(spec or (None, None)),
                                   g["bias"] if spec else None, s["hats"], s["score_ws"], s["scores"], st)
+                layer._after_read(reading)
                 L.veda_distill(lay, s["scores"], s["idx"], s["teacher"], s["cnt"], self.tau, s["loss"],
                                d_scores=s["d_scores"], row_weight=s["weight"], by_column=True, stream=st)
                 L.veda_score_backward(lay, s["feats_q"], s["feats_k"], s["hats"], s["d_scores"], s["back_ws"], s["d_q"],

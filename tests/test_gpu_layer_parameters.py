@@ -89,6 +89,24 @@ def test_a_forward_elsewhere_waits_for_the_parameters():
     assert torch.equal(out, m.outs[1])
 
 
+def test_streams_by_handle_and_streams_that_are_gone():
+    # a stream as its handle, made and destroyed by its owner between two changes of the parameters
+    m = Made(direct=True)
+    rt = C.CDLL("libcudart.so.12")
+    for i in (0, 1):
+        m.set(m.sets[i])
+        handle = C.c_void_p()
+        assert rt.cudaStreamCreate(C.byref(handle)) == 0
+        out = m.forward(handle.value)
+        assert rt.cudaStreamSynchronize(handle) == 0
+        assert torch.equal(out, m.outs[i])
+        assert rt.cudaStreamDestroy(handle) == 0
+    m.layer.set_bias()
+    m.layer.set_bias((2, 2, 2), FAR, torch.ones(m.layer.heads, 29))
+    m.forward()
+    torch.cuda.synchronize()
+
+
 def test_a_queued_step_keeps_the_parameters_it_was_called_with():
     m, side = Made(), torch.cuda.Stream()
     trainer = PredictorTrainer(m.layer)
