@@ -436,8 +436,8 @@ int veda_attend_int8_paired(const veda_layout* layout, const void* q_codes, cons
  *     teacher[h, i, j] = max over real rows r of tile i and s of tile j of  D^-0.5 q_r . k_s - lse_r.
  *  q_t, k_t  device bf16 [n_heads, N, D] tile order (from veda_gather).
  *  row_lse   device fp32 [n_heads, S] at packed rows: the logarithm of each row's softmax sum, which makes the
- *            entries logarithms of max-pooled attention probabilities; NULL pools the logits themselves (lse = 0). Rows whose lse is not finite are passed over, and so
- *            are NaN logits; -inf where nothing is left.
+ *            entries logarithms of max-pooled attention probabilities; NULL pools the logits themselves (lse = 0).
+ *            Rows whose lse is not finite are passed over, and so are NaN logits; -inf where nothing is left.
  *  teacher   device fp32 [n_heads, n_video, n_video] out. */
 int veda_teacher(const veda_layout* layout, const void* q_t, const void* k_t, int32_t n_heads, int32_t dim,
                  const float* row_lse, float* teacher, void* stream);
@@ -465,7 +465,8 @@ int veda_bias_index(const veda_layout* layout, const veda_bias_spec* spec, int32
  *     scores[h, i, j] = q_hat_i . k_hat_j / sqrt(D) + bias[h, bucket(i, j)],
  * keeping the projected features for veda_score_backward.
  *  spec, bias  the buckets, and device fp32 [n_heads, buckets]; both NULL: no bias. -inf keeps a bucket's pairs from
- *              being selected; finite values are taken no larger than 2^120 in magnitude.
+ *              being selected (but a row's own tile always is); finite values are taken no larger than 2^120 in
+ *              magnitude.
  *  hats        device fp32 [2, n_heads, n_video, D] out: q_hat, then k_hat.
  *  workspace   at least veda_score_bias_workspace_bytes().
  * Other arguments and errors as veda_score. */

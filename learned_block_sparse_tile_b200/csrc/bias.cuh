@@ -125,9 +125,9 @@ __device__ __forceinline__ void bias_interval(const int* starts, int reach, int 
 // (104k rows, 24 heads, from HBM: 44 -> 32 us). At the end each bucket is the sum of a box of offsets, taken axis by axis:
 // a box may hold nearly all offsets, and one chain of them would lose what a few long ones do not. Bound by the chain
 // of shared-memory addition and barrier, with up to three CTAs on an SM taking turns (104k, 24 heads: 28 us from HBM, 23
-// from L2; two CTAs: 32 and 24; two sets of sums and a barrier for each two rows gain nothing: 29 and 23); the floor is
-// reading d_scores once. With two values a thread the registers are held to three CTAs of any size (960 tiles, 24 heads: 36
-// us, two CTAs 40; 868 tiles 32, and 49 where the third waits for the others' end).
+// from L2, 31 in repeated calls from the host; two CTAs: 32 and 24; two sets of sums and a barrier for each two rows gain
+// nothing: 29 and 23); the floor is reading d_scores once. With two values a thread the registers are held to three CTAs of
+// any size (960 tiles, 24 heads: 36 us, two CTAs 40; 868 tiles 32, and 49 where the third waits for the others' end).
 template <int kPer, bool kOneSpan>
 __global__ void __launch_bounds__(512, kPer == 2 ? 3 : kPer <= 4 ? 2 : 1) bias_backward_kernel(const BiasBackwardArgs a) {
     constexpr int kDepth = kPer <= 2 ? 8 : kPer <= 4 ? 4 : 2;

@@ -68,7 +68,8 @@ __device__ __forceinline__ float row_sum(float v, float* scratch) {
 }
 
 // Rows of up to 32 * kPer * kWarps columns. One warp per row: four rows in a CTA; else one row in a CTA. The registers are
-// held to 72 a thread, 28 warps an SM: 220k rows, 24 heads take 112 us with 28 warps, 132 with 20 and 165 with 32 (spills).
+// held to 72 a thread, 28 warps an SM: 220k rows, 24 heads take 111 us with 28 warps, 132 with 20 and 165 with 32 (spills);
+// 121 in repeated calls from the host.
 template <int kPer, int kWarps>
 __global__ void __launch_bounds__(kWarps == 1 ? 128 : 32 * kWarps, kWarps == 1 ? 7 : kWarps == 2 ? 14 : 1) distill_kernel(const DistillArgs a) {
     constexpr int kLanes = 32 * kWarps;

@@ -7,8 +7,11 @@
 // the level of fp32 rounding as well: the tensor core truncates when it adds into its accumulator, so the errors of a
 // long sum all have one sign and add up. So the sums are cut at every slice of 32 values of K, and the epilogue warps add
 // the slices' sums in registers in rounded fp32; and a slice's small products go first, into an accumulator that is still
-// small. Scores of 819 tiles, 24 heads against 64 bits: 3.9e-6 with one accumulator, 1.0e-6 with sums of 64 values, 3.4e-7
-// with these (97 us instead of 95); fp32 products leave 5.4e-7.
+// small. Scores of 819 tiles, 24 heads against 64 bits: 3.9e-6 with one accumulator, 1.0e-6 with sums of 64 values, 3.3e-7
+// with these (97 us instead of 95 when it came in); fp32 products leave 4.5e-7.
+//
+// Times here are of runs of a few milliseconds, as each step was taken; the kernels now take 95 us (scores) and 97 us
+// (gradients, both launches), 98 and 110 in half a second of calls from the host.
 //
 // The projections' residual, feats @ P + feats[:, :D] = feats @ (P + E) with E the identity in P's first D rows, is added to
 // A as it is split.
@@ -244,7 +247,7 @@ __device__ __forceinline__ void read_quads(float (&v)[16], const uint8_t* raw, i
 // x rounded to the nearest tf32 value, ties away from zero, but no farther than the largest one: a finite value's remainder
 // stays finite, an infinity's carries it (its products are infinite as fp32's are, but NaN can come of a partner of 2^11 or
 // more, whose own remainder passes the type's range with the largest value), and a NaN's is NaN. The bound is the third of the
-// split's instructions (819 tiles, 24 heads: scores 93.5 -> 94.9 us, gradients 101.7 -> 104.0).
+// split's instructions (819 tiles, 24 heads: scores 93.7 -> 95.2 us, gradients 94.3 -> 97.0).
 __device__ __forceinline__ float hi_part(float x) {
     float r = __uint_as_float((__float_as_uint(x) + 0x1000u) & 0xffffe000u);
     asm("min.xorsign.abs.f32 %0, %0, 0f7F7FE000;" : "+f"(r));

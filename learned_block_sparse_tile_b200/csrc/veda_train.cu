@@ -141,7 +141,8 @@ constexpr size_t kSplitBytes = size_t(kSplitUnits) * train::kBM * train::kBN * s
 
 // Tiles past whole rounds of CTAs are cut along K into as many parts as CTAs are left, of at least kSplitSlices slices,
 // when that shortens the last round by more than joining the parts takes (about kJoinSlices slices' time). 819 tiles,
-// D 128, both gradients: 24 heads 96 -> 93 us, 8 heads 50 -> 46, 1 head 46 -> 24. More than one part takes a launch more.
+// D 128, both gradients in runs of a few milliseconds: 24 heads 96 -> 93 us, 8 heads 50 -> 46, 1 head 46 -> 24 (now 97 with
+// 24 heads: hi_part's bound). More than one part takes a launch more.
 int parts_along_k(int64_t tiles, int K, int sms) {
     const int nk = (K + train::kBK - 1) / train::kBK, rest = int(tiles % sms);
     const int parts = rest ? std::min(std::min(sms, kSplitUnits) / rest, nk / kSplitSlices) : 1;
@@ -206,11 +207,13 @@ int launch_distill(const DistillArgs& a, cudaStream_t s) {
     return launch_status("distill_kernel");
 }
 
-// Query rows of one chunk of the bias gradient's sums: with all heads as many CTAs for each of 148 SMs as can be
-// resident (their registers decide), but not fewer than eight rows, which a chunk's own start and end cost. Three against
-// two: 819 tiles, 24 heads 28 and 32 us, 480 tiles (a CTA too many) 24 and 16, 1860 tiles 110 and 82; two against one: 3720
-// tiles, 8 heads 103 and 130, 7320 tiles, 4 heads 231 and 205. Over 8192 tiles the kernel without offset sums runs, bound
-// by latency: 14,880 tiles 8.6, 3.2, 2.8 ms with one, three, six.
+// Query rows of one chunk of the bias gradient's sums: with all heads one to three CTAs (six of the kernel without offset
+// sums) for each of 148 SMs, but not fewer than eight rows, which a chunk's own start and end cost. How many is a table by
+// the row length, from what was measured with these kernels' registers, not what could be resident: at 128 tiles ten CTAs
+// would fit, at 1,100 four; and shared memory is not looked at, which lets in one CTA of 16 x 16 x 16 tiles (116 KB of
+// offset sums) where the table says two. Three against two: 819 tiles, 24 heads 28 and 32 us, 480 tiles (a CTA too many) 24
+// and 16, 1860 tiles 110 and 82; two against one: 3720 tiles, 8 heads 103 and 130, 7320 tiles, 4 heads 231 and 205. The
+// kernel without offset sums is bound by latency: 14,880 tiles, 2 heads 8.6, 3.2, 2.8 ms with one, three, six.
 int bias_chunk_rows(int n, int n_heads) {
     const int resident = n <= 1024 ? (n <= 416 || n > 512 ? 3 : 2) : n <= 4096 ? 2 : n <= 8192 ? 1 : 6;
     const int chunks = std::max(1, std::min(148 * resident / std::max(n_heads, 1), (n + 7) / 8));

@@ -10,7 +10,8 @@ rows' softmax sums are given; its top tiles under the layer's own budgets are th
     loss, grads = trainer.step()               # mean loss; gradients of proj_q, proj_k and bias
     ...                                        # the caller's optimizer, then layer.set_projections / set_bias
 
-PyTorch only allocates device buffers and supplies the stream; every step runs in libveda's kernels.
+The operators run in libveda's kernels; PyTorch allocates the buffers, supplies the stream, puts the groups' gradients into
+the layer's head order and sums the loss.
 """
 from __future__ import annotations
 
