@@ -425,7 +425,8 @@ int veda_attend_int8_paired(const veda_layout* layout, const void* q_codes, cons
  * All sums are fp32 or wider, nothing is atomic, and two calls on the same inputs give the same bits. The products of
  * veda_score_bias and veda_score_backward (split tf32, fp32 sums) take any finite fp32 value; a sum that passes the type's
  * range on its way is infinite or NaN. A NaN or an infinity reaches the outputs that its formula takes it to and no other:
- * a NaN as NaN, an infinity as it would in fp32, or as NaN where it meets a value of 2^11 or more.
+ * a NaN as NaN, an infinity as it would in fp32, or as NaN where the values that it and its like meet in a sum add up to
+ * 2^11 or more in magnitude.
  * Limits of every call here: 16384 video tiles and 65535 heads (VEDA_ERR_UNSUPPORTED beyond). Buffers need
  * 16-byte alignment. Outputs and workspaces must not overlap each other or a call's inputs. The first call that uses
  * a layout on a device uploads its index data (an allocation and a copy that waits): make it before any stream

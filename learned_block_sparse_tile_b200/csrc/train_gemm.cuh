@@ -245,9 +245,10 @@ __device__ __forceinline__ void read_quads(float (&v)[16], const uint8_t* raw, i
 }
 
 // x rounded to the nearest tf32 value, ties away from zero, but no farther than the largest one: a finite value's remainder
-// stays finite, an infinity's carries it (its products are infinite as fp32's are, but NaN can come of a partner of 2^11 or
-// more, whose own remainder passes the type's range with the largest value), and a NaN's is NaN. The bound is the third of the
-// split's instructions (819 tiles, 24 heads: scores 93.7 -> 95.2 us, gradients 94.3 -> 97.0).
+// stays finite, an infinity's carries it, and a NaN's is NaN. Products with an infinity are then infinite as fp32's are; but
+// the largest value times a partner's remainder may pass the type's range with the other sign, and the sum is NaN, where the
+// partners add up to 2^11 or more. The bound is the third of the split's instructions (819 tiles, 24 heads: scores 93.7 ->
+// 95.2 us, gradients 94.3 -> 97.0).
 __device__ __forceinline__ float hi_part(float x) {
     float r = __uint_as_float((__float_as_uint(x) + 0x1000u) & 0xffffe000u);
     asm("min.xorsign.abs.f32 %0, %0, 0f7F7FE000;" : "+f"(r));
