@@ -190,3 +190,47 @@ def test_a_layer_counts_the_launches_it_makes(dim, heads, grid):
         assert layer.launches == kernel_nodes(lambda: layer.forward(q, k, v, out))
     layer.set_bias()
     assert layer.launches == plain == kernel_nodes(lambda: layer.forward(q, k, v, out))
+
+
+def test_a_captured_step_follows_the_parameters_and_the_teacher():
+    m = Made()
+    trainer = PredictorTrainer(m.layer)
+    inputs = [(m.q, m.k), (m.k, m.q)]
+    want = {}
+    for i in (0, 1):
+        for j in (0, 1):
+            m.set(m.sets[i])
+            trainer.teach(*inputs[j])
+            loss, grads = trainer.step()
+            want[i, j] = loss.clone(), {x: grads[x].clone() for x in grads}
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        loss, grads = trainer.step()
+    for i, j in ((0, 0), (1, 0), (1, 1), (0, 1)):
+        m.set(m.sets[i])
+        trainer.teach(*inputs[j])
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(loss, want[i, j][0]) and all(torch.equal(grads[x], want[i, j][1][x]) for x in grads)
+
+
+@pytest.mark.parametrize("fp8,int8", [(True, False), (False, True)])
+def test_a_bias_on_layers_of_8_bit_codes(fp8, int8):
+    wl = V.workload("small_d128")
+    q, k, v = (x.cuda() for x in V.make_qkv(wl))
+    layer = VedaLayer(wl.seq_len, wl.ref_spans, wl.target, wl.head_shapes, (wl.generated, wl.reference), wl.heads, wl.dim,
+                      fp8_qk=fp8, int8_qk=int8)
+    layer.set_projections(*V.make_projections(wl))
+    outs, kept = [], []
+    for bias in (None, torch.zeros(wl.heads, L.veda_bias_buckets(REACH, FAR)), 4 * torch.randn(wl.heads, L.veda_bias_buckets(REACH, FAR))):
+        layer.set_bias(*((None, None, None) if bias is None else (REACH, FAR, bias)))
+        out = torch.zeros(wl.seq_len, wl.heads, wl.dim, dtype=torch.bfloat16, device="cuda")
+        layer.forward(q, k, v, out)
+        torch.cuda.synchronize()
+        outs.append(out)
+        kept.append([g["kept_cnt"].clone() for g in layer.groups])
+        assert bool(torch.isfinite(out.float()).all())
+    # the budgets stay, what is kept under them changes with a bias that is not zero
+    assert all(torch.equal(a, b) for other in kept[1:] for a, b in zip(kept[0], other))
+    assert not torch.equal(outs[0], outs[2])
